@@ -1,0 +1,621 @@
+// Causal softmax attention over packed sequences with grouped heads, on tcgen05.
+//
+// For row r of sequence i (nq queries, nk keys; the last query stands at the
+// last key) and query head h of key head h / G:
+//   o_r = sum_{j <= nk - nq + r} p_rj v_j,  p_rj = exp(s q_r.k_j) / l_r
+// and lse_r = log l_r. A row that sees no key gives 0 and -inf.
+//
+// Tiles. A tile is 128 rows: 128 / G tokens times the G query heads that share
+// one key head, packed (token, head), so that a key block is read once for the
+// whole group and a diagonal block wastes 128 / G tokens only. Rows are
+// independent in every product, so rows that do not exist (G not dividing 128,
+// tokens past the sequence) carry what lies there and are not stored.
+//
+// One CTA runs two streams of softmax rows, each with its own four warps, its own
+// logits S and its own accumulator O in TMEM (S 2 x 128 columns, O 2 x D; the
+// probabilities overwrite their logits as packed bf16), so that the tensor cores
+// work on one stream's products while the other's exponentials run:
+//  - prompts: the streams are two consecutive tiles and share each key block;
+//  - few rows on long keys (single new tokens): both streams are the same tile,
+//    stream s takes key blocks s, s + 2, ... of this CTA's share of the keys, and
+//    each leaves a partial (o normalised by its own l, its log-sum) that a second
+//    kernel joins.
+//
+// Per key block: S = Q K^T (M = 128, N = 128), m = running row maximum in the
+// log2 domain, P = 2^(S s log2(e) - m) rounded to bf16 (the tensor cores' operand
+// type; the row sum l is taken over the unrounded values, so a weight is off by
+// half a bf16 step at most), O += P V. O is rescaled only where a row's maximum
+// grew by more than 2^8.
+//
+// Masks select: a masked logit becomes -inf whatever it was, and value rows past
+// a sequence's end are zeroed in shared memory before the product that reads
+// them, so neither infinities nor NaN behind a sequence reach a result. Within a
+// sequence, values are expected to be finite.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "seq.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace vda {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 320;  // TMA warp, MMA warp, two streams of four softmax warps
+constexpr int kMinSplitBlocks = 4;
+
+template <int D>
+struct CaCfg {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kRing = D == 128 ? 5 : 10;  // key and value blocks in flight, one ring
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 256 + D;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t kIdescO = sm100::idesc_bf16_f32(128, D, false, true);
+  static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may use");
+};
+
+struct CaArgs {
+  int N, Hkv, G, tpt;  // tpt: tokens per tile, 128 / G
+  int Tq, Tk;
+  int nsplit;          // shares of the keys (split form)
+  const int *cu_q, *cu_k, *k_len;
+  float sl;            // scale * log2(e)
+  __nv_bfloat16* O;
+  long long o_row;
+  float* lse;          // [Tq, Hq], nullable
+  float* part_o;       // split form: [2 nsplit][Tq * Hq][D]
+  float* part_l;       // split form: [2 nsplit][Tq * Hq], log2 domain
+  uint32_t* status;
+  unsigned long long wait_ns;
+};
+
+// Keys of sequence i: first token and count (k_len, where given, is the filled
+// part of the sequence's room).
+__device__ __forceinline__ void key_range(const CaArgs& a, int i, int& lo, int& n) {
+  int hi;
+  seq::bounds(a.cu_k, i, a.Tk, lo, hi);
+  n = hi - lo;
+  if (a.k_len) n = min(n, max(__ldg(a.k_len + i), 0));
+}
+
+// How many of nsplit shares a tile of nb key blocks uses (a share of fewer than
+// kMinSplitBlocks blocks costs more to start than it saves), and share z of them.
+__device__ __forceinline__ int used_splits(int nb, int nsplit) {
+  return max(1, min(nsplit, (nb + kMinSplitBlocks - 1) / kMinSplitBlocks));
+}
+
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    causal_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                          const __grid_constant__ CUtensorMap mV, const CaArgs a) {
+  using C = CaCfg<D>;
+  using namespace sm100;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint8_t* sQ = smem + C::kQOff;
+  uint8_t* sR = smem + C::kRingOff;
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* rfull = qfull + 1;
+  uint64_t* rempty = rfull + C::kRing;
+  uint64_t* sfull = rempty + C::kRing;  // [2] logits of stream s in TMEM
+  uint64_t* pfull = sfull + 2;          // [2] probabilities of stream s in TMEM
+  uint64_t* pvdone = pfull + 2;         // [2] O of stream s accumulated
+  uint64_t* drain = pvdone + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
+  static_assert((1 + 2 * C::kRing + 7) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int hk = blockIdx.x % a.Hkv;
+  const int rest = blockIdx.x / a.Hkv;
+  const int z = kSplit ? rest % a.nsplit : 0;
+  const int per_item = kSplit ? a.tpt : 2 * a.tpt;
+  int idx;
+  const int sq = seq::find_item(
+      kSplit ? rest / a.nsplit : rest, a.N, scratch,
+      [&](int i) {
+        int lo, hi;
+        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
+        return (hi - lo + per_item - 1) / per_item;
+      },
+      idx);
+  if (sq < 0) return;
+  int q_lo, q_hi, k_lo, nk;
+  seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
+  key_range(a, sq, k_lo, nk);
+  const int nq = q_hi - q_lo;
+  // Longest tiles first: a sequence's last rows see the most keys.
+  idx = (nq + per_item - 1) / per_item - 1 - idx;
+  // Per stream: first token within the sequence and key blocks seen.
+  int t0[2], nb[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    t0[s] = idx * per_item + (kSplit ? 0 : s * a.tpt);
+    const int last = min(t0[s] + a.tpt, nq) - 1;
+    const int seen = t0[s] < nq ? min(nk, max(0, nk - nq + last + 1)) : 0;
+    nb[s] = (seen + kTile - 1) / kTile;
+  }
+  int b_lo = 0;  // first key block of this CTA's share
+  if (kSplit) {
+    const int used = used_splits(nb[0], a.nsplit);
+    if (z >= used) return;
+    b_lo = (int)((long long)nb[0] * z / used);
+    const int n = (int)((long long)nb[0] * (z + 1) / used) - b_lo;
+    nb[0] = (n + 1) / 2;
+    nb[1] = n / 2;
+  }
+  const int nb_all = kSplit ? nb[0] + nb[1] : max(nb[0], nb[1]);
+
+  if (warp == 0 && lane == 0) {
+    mbar_init(qfull, 1);
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&pvdone[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&mQ);
+    prefetch_tmap(&mK);
+    prefetch_tmap(&mV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int issued = 0;        // ring copies issued (producer only)
+  bool q_issued = false;
+
+  if (warp == 0) {
+    // ---------------- TMA producer. Ring order is the order in which the MMA
+    // warp takes blocks: K0 (K1 in the split form, one per stream), then V_t and
+    // the next K in turn.
+    if (lane == 0 && nb_all > 0) {
+      const uint32_t q_bytes = (uint32_t)(a.tpt * a.G) * 128u;
+      const int tiles = (!kSplit && nb[1] > 0) ? 2 : 1;
+      mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * tiles);
+      for (int s = 0; s < tiles; ++s)
+#pragma unroll
+        for (int at = 0; at < C::kAtoms; ++at)
+          tma_load_3d(sQ + s * C::kTileBytes + at * (kTile * 128), &mQ, qfull, at * 64, hk * a.G, q_lo + t0[s]);
+      q_issued = true;
+      auto load = [&](const CUtensorMap* m, int blk) -> bool {
+        const int slot = issued % C::kRing;
+        if (!mbar_wait(&rempty[slot], ((issued / C::kRing) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) return false;
+        mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+#pragma unroll
+        for (int at = 0; at < C::kAtoms; ++at)
+          tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), m, &rfull[slot], at * 64, hk,
+                      k_lo + (b_lo + blk) * kTile);
+        ++issued;
+        return true;
+      };
+      constexpr int ahead = kSplit ? 2 : 1;
+      bool ok = load(&mK, 0);
+      if (kSplit && ok && nb_all > 1) ok = load(&mK, 1);
+      for (int t = 0; t < nb_all && ok; ++t) {
+        ok = load(&mV, t);
+        if (ok && t + ahead < nb_all) ok = load(&mK, t + ahead);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer. Products of one thread run in issue order, so
+    // the next S of a stream, issued after P V of the last, cannot overwrite the
+    // probabilities that product reads.
+    if (lane == 0) {
+      bool ok = nb_all == 0 || mbar_wait(qfull, 0, abort_flag, a.status, a.wait_ns);
+      int taken = 0;  // ring position
+      auto take = [&](int& slot) -> bool {
+        slot = taken % C::kRing;
+        const bool r = mbar_wait(&rfull[slot], (taken / C::kRing) & 1, abort_flag, a.status, a.wait_ns);
+        ++taken;
+        return r;
+      };
+      auto issue_s = [&](int s, int slot) {
+        const uint32_t qb = smem_u32(sQ + (kSplit ? 0 : s) * C::kTileBytes);
+        const uint32_t kb = smem_u32(sR + slot * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
+          mma_f16(tmem + (s ? C::kS1 : C::kS0), smem_desc_sw128(qb + off, 16, 1024),
+                  smem_desc_sw128(kb + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sfull[s]);
+      };
+      auto issue_pv = [&](int s, int j, int slot) -> bool {
+        if (!mbar_wait(&pfull[s], j & 1, abort_flag, a.status, a.wait_ns)) return false;
+        tc_fence_after();
+        const uint32_t vb = smem_u32(sR + slot * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8,
+                     smem_desc_sw128(vb + kk * 2048, kTile * 128, 1024), C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&pvdone[s]);
+        return true;
+      };
+      int slot = 0, vslot = 0;
+      if (ok && nb_all > 0) {
+        if (kSplit) {
+          for (int s = 0; s < min(2, nb_all) && ok; ++s) {
+            if (!(ok = take(slot))) break;
+            issue_s(s, slot);
+            mma_commit(&rempty[slot]);
+          }
+          for (int t = 0; t < nb_all && ok; ++t) {
+            if (!(ok = take(vslot)) || !(ok = issue_pv(t & 1, t >> 1, vslot))) break;
+            mma_commit(&rempty[vslot]);
+            if (t + 2 < nb_all) {
+              if (!(ok = take(slot))) break;
+              issue_s(t & 1, slot);
+              mma_commit(&rempty[slot]);
+            }
+          }
+        } else {
+          if ((ok = take(slot))) {
+            for (int s = 0; s < 2; ++s)
+              if (nb[s] > 0) issue_s(s, slot);
+            mma_commit(&rempty[slot]);
+          }
+          for (int i = 0; i < nb_all && ok; ++i) {
+            if (!(ok = take(vslot))) break;
+            bool have = false;
+            for (int s = 0; s < 2 && ok; ++s) {
+              if (i < nb[s] && !(ok = issue_pv(s, i, vslot))) break;
+              if (s == 1) mma_commit(&rempty[vslot]);
+              if (i + 1 < nb[s]) {
+                if (!have && !(ok = take(slot))) break;
+                have = true;
+                issue_s(s, slot);
+              }
+            }
+            if (ok && have) mma_commit(&rempty[slot]);
+          }
+        }
+      }
+      mma_commit(drain);
+    }
+  } else {
+    // ---------------- softmax and epilogue: stream s, one row per thread
+    const int s = (warp - 2) / 4;
+    const int quad = warp % 4;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int my_nb = nb[s];
+    const int tok = t0[s] + r / a.G;  // row's token within the sequence
+    const int head = hk * a.G + r % a.G;
+    const bool live = r < a.tpt * a.G && tok < nq;
+    const int lim = min(nk, nk - nq + tok + 1);  // keys this row sees
+    const bool any_live = quad * 32 < min(a.tpt, nq - t0[s]) * a.G;  // some row of this warp exists
+    const int min_lim = nk - nq + t0[s] + 1;                         // keys the tile's first row sees
+    const uint32_t sa = tmem + lane_off + (s ? C::kS1 : C::kS0);
+    const uint32_t oa = tmem + lane_off + (s ? C::kO1 : C::kO0);
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool w = mbar_wait(bar, parity, abort_flag, a.status, a.wait_ns);
+      return __all_sync(0xffffffffu, w);
+    };
+    for (int j = 0; j < my_nb; ++j) {
+      const int blk = kSplit ? b_lo + 2 * j + s : j;
+      const int k0 = blk * kTile;
+      if (!warp_wait(&sfull[s], j & 1)) { ok = false; break; }
+      tc_fence_after();
+      if (any_live) {
+        float x[kTile];
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t v[32];
+          seq::tmem_ld32(sa + c4 * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[c4 * 32 + k] = __uint_as_float(v[k]);
+        }
+        if (k0 + kTile > min_lim) {
+          const int n = lim - k0;
+#pragma unroll
+          for (int k = 0; k < kTile; ++k)
+            if (k >= n) x[k] = -INFINITY;
+        }
+        float mx[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) mx[q] = x[q];
+#pragma unroll
+        for (int k = 8; k < kTile; ++k) mx[k & 7] = fmaxf(mx[k & 7], x[k]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], mx[q + 4]);
+        const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl;
+        const bool grow = j > 0 && mb > m_run + 8.f;
+        if (j == 0) m_run = mb;
+        if (__any_sync(0xffffffffu, grow)) {
+          if (!warp_wait(&pvdone[s], (j - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const float f = grow ? seq::ex2_approx(m_run - mb) : 1.f;
+#pragma unroll
+          for (int c4 = 0; c4 < D / 32; ++c4) {
+            uint32_t v[32];
+            seq::tmem_ld32(oa + c4 * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = v[q * 16 + k];
+              tmem_st16(oa + c4 * 32 + q * 16, w);
+            }
+          }
+          if (grow) {
+            l_run *= f;
+            m_run = mb;
+          }
+        }
+        // A row that has seen no key yet keeps m = -inf; its weights are 0.
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        const float2 sl2 = make_float2(a.sl, a.sl), nm2 = make_float2(-m_use, -m_use);
+        float2 ls2[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ls2[q] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 y = __ffma2_rn(make_float2(x[c4 * 32 + 2 * k], x[c4 * 32 + 2 * k + 1]), sl2, nm2);
+            const float p0 = seq::ex2_approx(y.x), p1 = seq::ex2_approx(y.y);
+            ls2[k & 3] = __fadd2_rn(ls2[k & 3], make_float2(p0, p1));
+            w[k] = seq::pack_bf16(p0, p1);
+          }
+          tmem_st16(sa + c4 * 16, w);
+        }
+        l_run += ((ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y)) + ((ls2[2].x + ls2[2].y) + (ls2[3].x + ls2[3].y));
+        tmem_st_wait();
+      }
+      if (k0 + kTile > nk) {
+        // The keys end inside this block: zero the value rows behind them. The
+        // block's ring position follows from the loading order; its copy must
+        // have landed first.
+        const int t = 2 * j + s;
+        const int pos = kSplit ? t + min(t + 2, nb_all) : 2 * j + 1;
+        const int slot = pos % C::kRing;
+        if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { ok = false; break; }
+        if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[s]);
+    }
+    // ---------------- epilogue
+    const bool have = my_nb > 0;
+    if (ok && (!have || warp_wait(&pvdone[s], (my_nb - 1) & 1))) {
+      tc_fence_after();
+      const bool seen = l_run > 0.f;
+      const float inv = seen ? 1.f / l_run : 0.f;
+      const long long tok_g = (long long)q_lo + (live ? tok : 0);
+      const long long rows = (long long)a.Tq * a.Hkv * a.G;
+      const long long row = tok_g * a.Hkv * a.G + head;
+      if (kSplit) {
+        const long long at = (long long)(2 * z + s) * rows + row;
+        if (live) a.part_l[at] = seen ? m_run + log2f(l_run) : -INFINITY;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D);
+        if (any_live && have) {
+#pragma unroll
+          for (int c4 = 0; c4 < D / 32; ++c4) {
+            uint32_t v[32];
+            seq::tmem_ld32(oa + c4 * 32, v);
+            tmem_ld_wait();
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                dst[c4 * 8 + k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                                              __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+            }
+          }
+        }
+      } else {
+        if (live && a.lse) a.lse[row] = seen ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+        uint4* dst = reinterpret_cast<uint4*>(a.O + tok_g * a.o_row + (long long)head * D);
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t v[32];
+          seq::tmem_ld32(oa + c4 * 32, v);
+          tmem_ld_wait();
+          if (!live) continue;
+#pragma unroll
+          for (int q8 = 0; q8 < 4; ++q8) {
+            uint32_t op[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              op[k] = seen ? seq::pack_bf16(__uint_as_float(v[q8 * 8 + 2 * k]) * inv,
+                                            __uint_as_float(v[q8 * 8 + 2 * k + 1]) * inv)
+                           : 0u;
+            dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // Let every issued copy land before the CTA's shared memory is released.
+    if (q_issued) mbar_wait(qfull, 0, nullptr, a.status, a.wait_ns);
+    for (int i = max(0, issued - C::kRing); i < issued; ++i)
+      mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
+  }
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the partials of the split form: one warp per row (token, query head).
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
+  const int Hq = a.Hkv * a.G;
+  const long long rows = (long long)a.Tq * Hq;
+  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= rows) return;
+  const int tok = (int)(row / Hq), head = (int)(row % Hq);
+  if (tok < __ldg(a.cu_q) || tok >= __ldg(a.cu_q + a.N)) return;  // behind the last sequence: left as it was
+  // The row's sequence: the last one that starts at or before it.
+  int lo = 0, hi = a.N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (__ldg(a.cu_q + mid) <= tok) lo = mid;
+    else hi = mid - 1;
+  }
+  int q_lo, q_hi, k_lo, nk;
+  seq::bounds(a.cu_q, lo, a.Tq, q_lo, q_hi);
+  key_range(a, lo, k_lo, nk);
+  const int nq = q_hi - q_lo;
+  const int last = min((tok - q_lo) / a.tpt * a.tpt + a.tpt, nq) - 1;
+  const int nb = (min(nk, max(0, nk - nq + last + 1)) + kTile - 1) / kTile;
+  const int n = 2 * used_splits(nb, a.nsplit);
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_l[i * rows + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  constexpr int kPer = D / 32;
+  float acc[kPer], w_all = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  if (m > -INFINITY) {
+    for (int i = 0; i < n; ++i) {
+      const float l = a.part_l[i * rows + row];
+      if (l == -INFINITY) continue;  // a share without visible keys has written no o
+      const float w = exp2f(l - m);
+      w_all += w;
+      const float* src = a.part_o + (i * rows + row) * D + lane * kPer;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, src[k], acc[k]);
+    }
+  }
+  const float inv = w_all > 0.f ? 1.f / w_all : 0.f;
+  __nv_bfloat16* dst = a.O + (long long)tok * a.o_row + (long long)head * D + lane * kPer;
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[row] = m > -INFINITY ? (m + log2f(w_all)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The form and the number of key shares for a call. Prompts fill the GPU with
+// tiles; where two-tile CTAs are fewer than the SMs and the keys are longer than
+// the rows are many, the keys are shared out instead, in enough shares to give
+// each SM several CTAs (sequences differ in length, and a CTA takes one share).
+struct Plan {
+  bool split;
+  int nsplit;
+};
+Plan plan_of(const vda_attention_config& c) {
+  const int G = c.Hq / c.Hkv, tpt = kTile / G;
+  const long long tiles = ((long long)c.Tq / tpt + c.N) * c.Hkv;
+  const long long ctas = ((long long)c.Tq / (2 * tpt) + (c.N + 1) / 2) * c.Hkv;
+  const long long keys = (long long)c.Tk / c.N;  // mean room per sequence
+  Plan p{false, 1};
+  const long long rows = (long long)c.Tq / c.N;
+  const bool few = (long long)c.Tq <= (long long)c.N * tpt;  // about one tile per sequence
+  if (keys >= 2 * kMinSplitBlocks * kTile && (few || (ctas < 148 && keys >= 4 * rows))) {
+    p.split = true;
+    const long long want = (148LL * 8 + tiles - 1) / tiles;
+    const long long most = std::max(1LL, ((long long)c.Tk + kTile * kMinSplitBlocks - 1) / (kTile * kMinSplitBlocks));
+    p.nsplit = (int)std::max(1LL, std::min({want, most, 64LL}));
+  }
+  return p;
+}
+
+template <int D>
+cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K, const void* V, const int* cu_q,
+                     const int* cu_k, const int* k_len, void* O, float* lse, void* ws, uint32_t* status,
+                     cudaStream_t s) {
+  using C = CaCfg<D>;
+  const Plan p = plan_of(c);
+  CaArgs a{};
+  a.N = c.N; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.tpt = kTile / a.G; a.Tq = c.Tq; a.Tk = c.Tk;
+  a.nsplit = p.nsplit;
+  a.cu_q = cu_q; a.cu_k = cu_k; a.k_len = k_len;
+  a.sl = c.scale * 1.4426950408889634f;
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.o_row = c.o_row;
+  a.lse = lse;
+  const long long rows = (long long)c.Tq * c.Hq;
+  if (p.split) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_l = a.part_o + 2LL * p.nsplit * rows * D;
+  }
+  a.status = status;
+  a.wait_ns = 2000000000ull;
+  const int per_item = p.split ? a.tpt : 2 * a.tpt;
+  // ceil(n / per_item) summed over the sequences is at most Tq / per_item + N.
+  const long long items = (long long)c.Tq / per_item + c.N;
+  const long long grid = items * c.Hkv * p.nsplit;
+  if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+  const void* fn = p.split ? reinterpret_cast<const void*>(causal_attn_tc_kernel<D, true>)
+                           : reinterpret_cast<const void*>(causal_attn_tc_kernel<D, false>);
+  cudaError_t e = set_max_dynamic_smem(fn, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  uint64_t qdims[3] = {(uint64_t)D, (uint64_t)c.Hq, (uint64_t)c.Tq};
+  uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)c.q_row * 2};
+  uint32_t qbox[3] = {64, (uint32_t)a.G, (uint32_t)a.tpt};
+  // Without keys nothing is loaded from K and V: their maps describe one row of Q.
+  const bool none = c.Tk == 0;
+  uint64_t kdims[3] = {(uint64_t)D, (uint64_t)c.Hkv, (uint64_t)(none ? 1 : c.Tk)};
+  uint64_t kstr[2] = {(uint64_t)D * 2, (uint64_t)(none ? c.q_row : c.k_row) * 2};
+  uint64_t vstr[2] = {(uint64_t)D * 2, (uint64_t)(none ? c.q_row : c.v_row) * 2};
+  uint32_t kbox[3] = {64, 1, (uint32_t)kTile};
+  CUtensorMap mQ, mK, mV;
+  if ((e = make_tmap_bf16(&mQ, Q, 3, qdims, qstr, qbox)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16(&mK, none ? Q : K, 3, kdims, kstr, kbox)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16(&mV, none ? Q : V, 3, kdims, vstr, kbox)) != cudaSuccess) return e;
+  if (p.split) {
+    causal_attn_tc_kernel<D, true><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attn_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
+  } else {
+    causal_attn_tc_kernel<D, false><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t causal_attention_workspace(const vda_attention_config& c) {
+  const Plan p = plan_of(c);
+  if (!p.split) return 0;
+  return (size_t)2 * p.nsplit * c.Tq * c.Hq * (c.d + 1) * sizeof(float);
+}
+
+cudaError_t launch_causal_attention(const vda_attention_config& c, const void* Q, const void* K, const void* V,
+                                    const int* cu_q, const int* cu_k, const int* k_len, void* O, float* lse, void* ws,
+                                    uint32_t* status, cudaStream_t s) {
+  return c.d == 128 ? launch_d<128>(c, Q, K, V, cu_q, cu_k, k_len, O, lse, ws, status, s)
+                    : launch_d<64>(c, Q, K, V, cu_q, cu_k, k_len, O, lse, ws, status, s);
+}
+
+}  // namespace vda

@@ -1,0 +1,755 @@
+// Linear attention whose state decays by a factor of each head, over packed
+// sequences, on tcgen05: whole prompts, and the three passes of the backward.
+//
+//   S_t = a S_{t-1} + v_t k_t^T   (d_v x d_k, fp32),   o_t = s S_t q_t,   a = exp(log_decay[head]).
+//
+// In chunks of 128 tokens (n in the last), with X the state before the chunk,
+//   o_i = s [ sum_{j <= i} a^(i-j) (q_i.k_j) v_j + a^(i+1) X q_i ],
+//   X'  = a^n X + sum_j a^(n-1-j) v_j k_j^T.
+//
+// The gradients have the same form. With D_t = s do_t q_t^T + a D_{t+1}
+// (D_T = s do_T q_T^T + dS):
+//   dq_t = s S_t^T do_t   runs forward  with (q, k, v) := (do, v, k), state S0^T,
+//   dk_t = D_t^T v_t      runs backward with (v, do, q), state dS^T,
+//   dv_t = D_t k_t        runs backward with (k, q, do), state dS; its last state
+// is dS0. A pass that runs backward carries R_t = a D_t (the state is decayed
+// when it leaves a token, not when it enters the next), so with i counted from
+// the sequence's end its factors are a^i on the state and a^(n-j) on the update.
+// One kernel takes a list of such passes ("jobs"); the three of a backward run
+// in one launch and share their tensors' reads through L2.
+//
+// One CTA takes one (sequence, head, job, segment) and walks the segment's
+// chunks with X in registers. Per chunk: S1 = Q K^T and, masked and weighted,
+// P = bf16 in TMEM; O1 = P V; O2 = Q X^T with X rounded to bf16 in shared memory
+// (operand type of the tensor cores; outputs are bf16, so each of the two
+// roundings adds what the output's own rounding is); W = V'^T K, where
+// V' = a^(n-1-j) v_j enters as three bf16 parts (24 bits together), so that the
+// state, which is fp32 outside, keeps fp32 accuracy. W starts from zero in every
+// chunk and is added to X in registers: the tensor cores' accumulation rounds
+// toward zero, and over a long sequence that would pull the state down.
+//
+// What bounds it: the tensor work of a chunk is 3072 cycles (QK, PV, QX, and
+// three W parts, each 512 at d = 128), its four tiles take about 5700 cycles of
+// the HBM rate's share of one SM, so the copies decide when enough CTAs run.
+// Where (sequences x heads) leave SMs idle, long sequences are cut into
+// segments: a first launch forms every segment's own state from K and V alone,
+// a small kernel joins them in order, and the main launch starts each segment
+// from its state.
+//
+// Warps: 0 TMA, 1 MMA, 2-5 P and output rows, 6-13 V' and the state (a row of X
+// per thread pair: warps 6-9 the first half of its columns, 10-13 the second).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "seq.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace vda {
+
+namespace {
+
+constexpr int kC = 128;        // tokens per chunk
+constexpr int kThreads = 448;
+constexpr int kStateThreads = 256;
+constexpr int kQuarter = 32;   // tokens of V' per step
+constexpr int kMaxJobs = 3;
+
+template <int D>
+struct DaCfg {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kTileBytes = kC * D * 2;
+  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr int kPartBytes = kQuarter * D * 2;  // one of the three parts of V'
+  static constexpr int kVpOff = kRing * kTileBytes;
+  static constexpr int kXOff = kVpOff + 3 * kPartBytes;
+  static constexpr int kBarOff = kXOff + (D * D * 2 < 8192 ? 8192 : D * D * 2);
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static constexpr uint32_t kS1 = 0, kO1 = 128, kO2 = 256, kW = 384;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t kIdescPV = sm100::idesc_bf16_f32(128, D, false, true);
+  static constexpr uint32_t kIdescQX = sm100::idesc_bf16_f32(128, D, false, false);
+  static constexpr uint32_t kIdescW = sm100::idesc_bf16_f32(128, D, true, true);
+  static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may use");
+};
+
+struct DaMaps {
+  CUtensorMap m[4];
+};
+
+struct DaJob {
+  int q, k, v;               // which map plays which part
+  int reverse;
+  int init_t;                // the initial state is read transposed
+  float s_in, s_state, s_up; // factors of P V, of X Q and of the update
+  const float* init;         // [N, H, d, d], nullable (zero)
+  float* last;               // [N, H, d, d], nullable
+  __nv_bfloat16* out;
+  long long out_row;
+};
+
+struct DaArgs {
+  int N, H, T, njobs;
+  int seg;                  // chunks per segment
+  const int* cu;
+  const float* log_decay;   // [H]
+  DaJob job[kMaxJobs];
+  float* seg_state;         // [items][H][njobs][d * d]
+  uint32_t* status;
+  unsigned long long wait_ns;
+};
+
+// a^e for the head's log2 decay g2 (finite, see head_decay).
+__device__ __forceinline__ float power(float g2, int e) { return exp2f(g2 * (float)e); }
+
+// log2 of the head's decay. From 2^-300 down a factor is 0 in fp32 whatever the
+// exponent, and -inf would give NaN at distance 0.
+__device__ __forceinline__ float head_decay(const DaArgs& a, int h) {
+  const float g = __ldg(a.log_decay + h) * 1.4426950408889634f;
+  return g < -300.f ? -300.f : g;
+}
+
+// Tokens [lo, hi) of the processing-order chunks [p0, p1) of a sequence of len tokens.
+__device__ __forceinline__ void chunk_tokens(int len, int reverse, int p0, int p1, int& lo, int& hi) {
+  const int nch = (len + kC - 1) / kC;
+  lo = reverse ? (nch - p1) * kC : p0 * kC;
+  hi = min(len, reverse ? (nch - p0) * kC : p1 * kC);
+}
+
+template <int D, bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid_constant__ DaMaps maps,
+                                                                    const __grid_constant__ DaArgs a) {
+  using C = DaCfg<D>;
+  using namespace sm100;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint8_t* sVp = smem + C::kVpOff;
+  uint8_t* sX = smem + C::kXOff;
+  uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* rempty = rfull + C::kRing;
+  uint64_t* sfull = rempty + C::kRing;
+  uint64_t* pfull = sfull + 1;
+  uint64_t* odone = pfull + 1;
+  uint64_t* oempty = odone + 1;
+  uint64_t* vpfull = oempty + 1;
+  uint64_t* vpempty = vpfull + 1;
+  uint64_t* wfull = vpempty + 1;
+  uint64_t* wempty = wfull + 1;
+  uint64_t* xfull = wempty + 1;
+  uint64_t* xempty = xfull + 1;
+  uint64_t* drain = xempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
+  static_assert((2 * C::kRing + 11) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int jb = blockIdx.x % a.njobs;
+  const int h = (blockIdx.x / a.njobs) % a.H;
+  const int item = blockIdx.x / a.njobs / a.H;
+  const DaJob& job = a.job[jb];
+  const int seg_tokens = a.seg * kC;
+  int part;
+  const int sq = seq::find_item(
+      item, a.N, scratch,
+      [&](int i) {
+        int lo, hi;
+        seq::bounds(a.cu, i, a.T, lo, hi);
+        return max(1, (hi - lo + seg_tokens - 1) / seg_tokens);  // an empty sequence still has a state
+      },
+      part);
+  if (sq < 0) return;
+  int lo, hi;
+  seq::bounds(a.cu, sq, a.T, lo, hi);
+  const int len = hi - lo;
+  const int nch_all = (len + kC - 1) / kC;
+  const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
+  if (kStateOnly && part == nparts - 1) return;  // nothing follows the last segment
+  const int p0 = part * a.seg, nch = min(nch_all, p0 + a.seg) - p0;
+  const int rev = job.reverse;
+  const float g2 = head_decay(a, h);
+  const long long st_off = ((long long)sq * a.H + h) * (D * D);
+  float* seg_state = a.seg_state ? a.seg_state + (((long long)item * a.H + h) * a.njobs + jb) * (D * D) : nullptr;
+  // First token (within the tensor) and token count of processing-order chunk c.
+  auto chunk = [&](int c, int& tok, int& n) {
+    const int cc = rev ? nch_all - 1 - (p0 + c) : p0 + c;
+    tok = lo + cc * kC;
+    n = min(kC, len - cc * kC);
+  };
+  constexpr int kTiles = kStateOnly ? 2 : 3;  // ring tiles per chunk: (Q,) K, V
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 1);
+    }
+    mbar_init(sfull, 1);
+    mbar_init(pfull, 4);
+    mbar_init(odone, 1);
+    mbar_init(oempty, 4);
+    mbar_init(vpfull, 8);
+    mbar_init(vpempty, 1);
+    mbar_init(wfull, 1);
+    mbar_init(wempty, 8);
+    mbar_init(xfull, 8);
+    mbar_init(xempty, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    if (!kStateOnly) prefetch_tmap(&maps.m[job.q]);
+    prefetch_tmap(&maps.m[job.k]);
+    prefetch_tmap(&maps.m[job.v]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int issued = 0;
+  auto wait1 = [&](uint64_t* bar, uint32_t n) -> bool {  // n-th phase of the barrier, n = 0, 1, ...
+    return mbar_wait(bar, n & 1, abort_flag, a.status, a.wait_ns);
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool { return __all_sync(0xffffffffu, wait1(bar, n)); };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int c = 0; c < nch && ok; ++c) {
+        int tok, n;
+        chunk(c, tok, n);
+        for (int u = 0; u < kTiles && ok; ++u) {
+          const int which = kStateOnly ? u + 1 : u;
+          const CUtensorMap* m = &maps.m[which == 0 ? job.q : which == 1 ? job.k : job.v];
+          const int slot = issued % C::kRing;
+          if (!(ok = wait1(&rempty[slot], issued / C::kRing + 1))) break;
+          mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_3d(smem + slot * C::kTileBytes + at * (kC * 128), m, &rfull[slot], at * 64, h, tok);
+          ++issued;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int c = 0; c < nch && ok; ++c) {
+        const int base = c * kTiles;
+        const int pq = base, pk = base + kTiles - 2, pv = base + kTiles - 1;
+        const int slot_q = pq % C::kRing, slot_k = pk % C::kRing, slot_v = pv % C::kRing;
+        const uint32_t qb = smem_u32(smem + slot_q * C::kTileBytes);
+        const uint32_t kb = smem_u32(smem + slot_k * C::kTileBytes);
+        const uint32_t vb = smem_u32(smem + slot_v * C::kTileBytes);
+        // W += V'^T K over the 32 tokens of quarter q.
+        auto issue_w = [&](int q) -> bool {
+          if (!wait1(vpfull, 4 * c + q)) return false;
+          if (q == 0 && c > 0 && !wait1(wempty, c - 1)) return false;
+          tc_fence_after();
+          const uint32_t ab = smem_u32(sVp);
+#pragma unroll
+          for (int part3 = 0; part3 < 3; ++part3)
+#pragma unroll
+            for (int kk = 0; kk < kQuarter / 16; ++kk)
+              mma_f16(tmem + C::kW, smem_desc_sw128(ab + part3 * C::kPartBytes + kk * 2048, kQuarter * 128, 1024),
+                      smem_desc_sw128(kb + (q * 2 + kk) * 2048, kC * 128, 1024), C::kIdescW,
+                      (q > 0 || part3 > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(vpempty);
+          return true;
+        };
+        if (!(ok = wait1(&rfull[slot_k], pk / C::kRing))) break;
+        if (!kStateOnly) {
+          if (!(ok = wait1(&rfull[slot_q], pq / C::kRing))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
+            mma_f16(tmem + C::kS1, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
+                    C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(sfull);
+        }
+        if (!(ok = issue_w(0))) break;
+        if (!kStateOnly) {
+          if (!(ok = wait1(xfull, c))) break;
+          if (c > 0 && !(ok = wait1(oempty, c - 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
+            const uint32_t xoff = (kk / 4) * (D * 128) + (kk % 4) * 32;
+            mma_f16(tmem + C::kO2, smem_desc_sw128(qb + off, 16, 1024),
+                    smem_desc_sw128(smem_u32(sX) + xoff, 16, 1024), C::kIdescQX, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(xempty);
+          mma_commit(&rempty[slot_q]);
+        }
+        for (int q = 1; q < 4 && ok; ++q) ok = issue_w(q);
+        if (!ok) break;
+        mma_commit(wfull);
+        if (!kStateOnly) {
+          if (!(ok = wait1(pfull, c))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk)
+            mma_f16_ts(tmem + C::kO1, tmem + C::kS1 + kk * 8, smem_desc_sw128(vb + kk * 2048, kC * 128, 1024),
+                       C::kIdescPV, kk > 0 ? 1u : 0u);
+          mma_commit(odone);
+        }
+        mma_commit(&rempty[slot_k]);
+        mma_commit(&rempty[slot_v]);
+      }
+      mma_commit(drain);
+    }
+  } else if (warp < 6) {
+    // ---------------- P and the output rows: row i of the chunk per thread
+    if (!kStateOnly) {
+      const int quad = warp % 4;
+      const int i = quad * 32 + lane;
+      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      bool ok = true;
+      for (int c = 0; c < nch && ok; ++c) {
+        int tok, n;
+        chunk(c, tok, n);
+        if (!(ok = warp_wait(sfull, c))) break;
+        tc_fence_after();
+        // Weight a^|i - j| of the pairs this row sees: j <= i forward, i <= j < n backward.
+        const int j_lo = rev ? i : 0, j_hi = rev ? n : min(i + 1, n);
+        const float sg = rev ? g2 : -g2;
+        const float e0 = rev ? -g2 * (float)i : g2 * (float)i;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t v[32], w[16];
+          seq::tmem_ld32(tmem + lane_off + C::kS1 + c4 * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = c4 * 32 + 2 * k + e;
+              const float x = __uint_as_float(v[2 * k + e]) * seq::ex2_approx(fmaf(sg, (float)j, e0));
+              p[e] = (j >= j_lo && j < j_hi) ? x : 0.f;
+            }
+            w[k] = seq::pack_bf16(p[0], p[1]);
+          }
+          tmem_st16(tmem + lane_off + C::kS1 + c4 * 16, w);
+        }
+        tmem_st_wait();
+        if (n < kC) {
+          // Value rows behind the sequence are zeroed: 0 x NaN is NaN.
+          const int pv = c * kTiles + kTiles - 1;
+          if (!(ok = warp_wait(&rfull[pv % C::kRing], pv / C::kRing))) break;
+          if (i >= n) seq::zero_row(smem + (pv % C::kRing) * C::kTileBytes, C::kAtoms, i, kC);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+        // Output: o_i = s_in O1 + s_state a^(i+1) O2 (a^(distance from the end) backward).
+        const float f = job.s_state * power(g2, rev ? n - 1 - i : i + 1);
+        if (!(ok = warp_wait(odone, c))) break;
+        tc_fence_after();
+        uint4* dst = reinterpret_cast<uint4*>(job.out + (long long)(tok + min(i, n - 1)) * job.out_row + h * D);
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t v[32], x[32];
+          seq::tmem_ld32(tmem + lane_off + C::kO1 + c4 * 32, v);
+          seq::tmem_ld32(tmem + lane_off + C::kO2 + c4 * 32, x);
+          tmem_ld_wait();
+          if (i < n) {
+#pragma unroll
+            for (int q8 = 0; q8 < 4; ++q8) {
+              uint32_t op[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = q8 * 8 + 2 * k;
+                op[k] = seq::pack_bf16(fmaf(f, __uint_as_float(x[e]), job.s_in * __uint_as_float(v[e])),
+                                       fmaf(f, __uint_as_float(x[e + 1]), job.s_in * __uint_as_float(v[e + 1])));
+              }
+              dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
+      }
+    }
+  } else {
+    // ---------------- V' and the state
+    constexpr int kCols = D / 2;
+    const int st = threadIdx.x - (kThreads - kStateThreads);
+    const int half = (warp - 6) / 4;
+    const int quad = warp % 4;
+    const int row = quad * 32 + lane;  // row of X
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const bool has_row = row < D;
+    float X[kCols];
+    {
+      const bool joined = !kStateOnly && nparts > 1;
+      const float* src = kStateOnly ? nullptr : joined ? seg_state : job.init ? job.init + st_off : nullptr;
+      const bool tr = !joined && job.init_t;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) X[k] = 0.f;
+      if (src && has_row) {
+        if (tr) {
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) X[k] = src[(half * kCols + k) * D + row];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kCols; k += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + row * D + half * kCols + k);
+            X[k] = x.x;
+            X[k + 1] = x.y;
+            X[k + 2] = x.z;
+            X[k + 3] = x.w;
+          }
+        }
+      }
+    }
+    // X as the bf16 K-major operand of Q X^T: row (value channel) x 64-column atoms.
+    auto write_x = [&] {
+      if (has_row) {
+#pragma unroll
+        for (int k8 = 0; k8 < kCols / 8; ++k8) {
+          const int col = half * kCols + k8 * 8;
+          uint8_t* p = sX + (col / 64) * (D * 128) + row * 128 + ((((col % 64) / 8) ^ (row & 7)) * 16);
+          *reinterpret_cast<uint4*>(p) =
+              make_uint4(seq::pack_bf16(X[k8 * 8], X[k8 * 8 + 1]), seq::pack_bf16(X[k8 * 8 + 2], X[k8 * 8 + 3]),
+                         seq::pack_bf16(X[k8 * 8 + 4], X[k8 * 8 + 5]), seq::pack_bf16(X[k8 * 8 + 6], X[k8 * 8 + 7]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xfull);
+    };
+    bool ok = true;
+    if (!kStateOnly && nch > 0) write_x();
+    for (int c = 0; c < nch && ok; ++c) {
+      int tok, n;
+      chunk(c, tok, n);
+      const int pk = c * kTiles + kTiles - 2, pv = pk + 1;
+      uint8_t* vt = smem + (pv % C::kRing) * C::kTileBytes;
+      if (!(ok = warp_wait(&rfull[pv % C::kRing], pv / C::kRing))) break;
+      if (n < kC) {
+        if (!(ok = warp_wait(&rfull[pk % C::kRing], pk / C::kRing))) break;
+        if (st < kC && st >= n) seq::zero_row(smem + (pk % C::kRing) * C::kTileBytes, C::kAtoms, st, kC);
+      }
+      for (int q = 0; q < 4 && ok; ++q) {
+        const int vp = 4 * c + q;
+        // Eight threads to a token, D / 8 channels each.
+        const int tl = st / 8, j = q * kQuarter + tl;
+        constexpr int kCh = D / 64;  // 16-byte chunks per thread
+        uint4 raw[kCh];
+#pragma unroll
+        for (int u = 0; u < kCh; ++u) {
+          const int ch = (st % 8) * kCh + u;  // chunk of 8 channels
+          raw[u] = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kC * 128) + j * 128 + (((ch % 8) ^ (j & 7)) * 16));
+        }
+        const float w = j < n ? job.s_up * power(g2, rev ? j + 1 : n - 1 - j) : 0.f;
+        if (vp > 0 && !(ok = warp_wait(vpempty, vp - 1))) break;
+#pragma unroll
+        for (int u = 0; u < kCh; ++u) {
+          const int ch = (st % 8) * kCh + u;
+          const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          uint32_t out[3][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(bits_bf162(in[e]));
+            float x = j < n ? f.x * w : 0.f, y = j < n ? f.y * w : 0.f;
+#pragma unroll
+            for (int p3 = 0; p3 < 3; ++p3) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+              out[p3][e] = bf162_bits(b);
+              const float2 r = __bfloat1622float2(b);
+              x -= r.x;
+              y -= r.y;
+            }
+          }
+#pragma unroll
+          for (int p3 = 0; p3 < 3; ++p3)
+            *reinterpret_cast<uint4*>(sVp + p3 * C::kPartBytes + (ch / 8) * (kQuarter * 128) + tl * 128 +
+                                      (((ch % 8) ^ (tl & 7)) * 16)) =
+                make_uint4(out[p3][0], out[p3][1], out[p3][2], out[p3][3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vpfull);
+      }
+      if (!ok) break;
+      // X' = a^n X + W
+      if (!(ok = warp_wait(wfull, c))) break;
+      tc_fence_after();
+      const float f = power(g2, n);
+#pragma unroll
+      for (int k4 = 0; k4 < kCols / 32; ++k4) {
+        uint32_t v[32];
+        seq::tmem_ld32(tmem + lane_off + C::kW + half * kCols + k4 * 32, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) X[k4 * 32 + k] = fmaf(f, X[k4 * 32 + k], __uint_as_float(v[k]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wempty);
+      if (!kStateOnly && c + 1 < nch) {
+        if (!(ok = warp_wait(xempty, c))) break;  // Q X^T of this chunk has read the old X
+        write_x();
+      }
+    }
+    float* last = kStateOnly ? seg_state : (part == nparts - 1 && job.last) ? job.last + st_off : nullptr;
+    if (ok && last && has_row) {
+#pragma unroll
+      for (int k = 0; k < kCols; k += 4)
+        *reinterpret_cast<float4*>(last + row * D + half * kCols + k) = make_float4(X[k], X[k + 1], X[k + 2], X[k + 3]);
+    }
+  }
+
+  // ---------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    for (int i = max(0, issued - C::kRing); i < issued; ++i)
+      mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
+  }
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Turns each segment's own state into the state before it, in order, for the
+// sequences that have several: block (sequence, head, job) x slices of the matrix.
+template <int D>
+__global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DaArgs a) {
+  __shared__ int first_s;
+  const int sq = blockIdx.y;
+  const int jb = blockIdx.x % a.njobs, h = (blockIdx.x / a.njobs) % a.H;
+  const int slice = blockIdx.x / a.njobs / a.H;
+  const DaJob& job = a.job[jb];
+  const int seg_tokens = a.seg * kC;
+  int lo, hi;
+  seq::bounds(a.cu, sq, a.T, lo, hi);
+  const int len = hi - lo;
+  const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
+  if (nparts == 1) return;
+  if (threadIdx.x == 0) first_s = 0;
+  __syncthreads();
+  int before = 0;  // items of the sequences before this one
+  for (int i = threadIdx.x; i < sq; i += blockDim.x) {
+    int x, y;
+    seq::bounds(a.cu, i, a.T, x, y);
+    before += max(1, (y - x + seg_tokens - 1) / seg_tokens);
+  }
+  if (before) atomicAdd(&first_s, before);
+  __syncthreads();
+  const int e = (slice * 256 + threadIdx.x) * 4;
+  const int r = e / D, c = e % D;
+  const float g2 = head_decay(a, h);
+  const float* init = job.init ? job.init + ((long long)sq * a.H + h) * (D * D) : nullptr;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (init) {
+    if (job.init_t)
+      x = make_float4(init[c * D + r], init[(c + 1) * D + r], init[(c + 2) * D + r], init[(c + 3) * D + r]);
+    else
+      x = *reinterpret_cast<const float4*>(init + e);
+  }
+  const int nch = (len + kC - 1) / kC;
+  for (int p = 0; p < nparts; ++p) {
+    float4* w = reinterpret_cast<float4*>(
+        a.seg_state + (((long long)(first_s + p) * a.H + h) * a.njobs + jb) * (D * D) + e);
+    int t0, t1;
+    chunk_tokens(len, job.reverse, p * a.seg, min(nch, (p + 1) * a.seg), t0, t1);
+    const float4 y = p + 1 < nparts ? *w : make_float4(0.f, 0.f, 0.f, 0.f);
+    *w = x;
+    const float f = power(g2, t1 - t0);
+    x = make_float4(fmaf(f, x.x, y.x), fmaf(f, x.y, y.y), fmaf(f, x.z, y.z), fmaf(f, x.w, y.w));
+  }
+}
+
+// One token of every sequence: S <- a S + v k^T in place, o = s S q. Memory
+// bound: the state is read and written once. A warp takes rows of S (a value
+// channel each), a lane D / 32 key channels; kRows rows are in flight per warp.
+template <int D>
+__global__ void __launch_bounds__(256) decay_step_kernel(const vda_decay_config c, const __nv_bfloat16* Q,
+                                                         const __nv_bfloat16* K, const __nv_bfloat16* V,
+                                                         const float* log_decay, float* S, __nv_bfloat16* O,
+                                                         int slabs) {
+  constexpr int kPer = D / 32;
+  constexpr int kRows = 4;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int slab = blockIdx.x % slabs;
+  const long long nh = blockIdx.x / slabs;
+  const int h = (int)(nh % c.H);
+  const long long n = nh / c.H;
+  const float a = expf(__ldg(log_decay + h));
+  float k[kPer], q[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) {
+    const float2 kf = __bfloat1622float2(
+        *reinterpret_cast<const __nv_bfloat162*>(K + n * c.k_row + (long long)h * D + lane * kPer + e));
+    const float2 qf = __bfloat1622float2(
+        *reinterpret_cast<const __nv_bfloat162*>(Q + n * c.q_row + (long long)h * D + lane * kPer + e));
+    k[e] = kf.x;
+    k[e + 1] = kf.y;
+    q[e] = qf.x;
+    q[e + 1] = qf.y;
+  }
+  const int rows = D / slabs;
+  float* Sm = S + nh * (D * D);
+  const __nv_bfloat16* Vr = V + n * c.v_row + (long long)h * D;
+  __nv_bfloat16* Or = O + n * c.o_row + (long long)h * D;
+  for (int r0 = slab * rows + warp * kRows; r0 < (slab + 1) * rows; r0 += 8 * kRows) {
+    float x[kRows][kPer], o[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if constexpr (kPer == 4) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(Sm + (r0 + r) * D) + lane);
+        x[r][0] = f.x; x[r][1] = f.y; x[r][2] = f.z; x[r][3] = f.w;
+      } else {
+        const float2 f = __ldcs(reinterpret_cast<const float2*>(Sm + (r0 + r) * D) + lane);
+        x[r][0] = f.x; x[r][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float v = __bfloat162float(Vr[r0 + r]);
+      o[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        x[r][e] = fmaf(a, x[r][e], v * k[e]);
+        o[r] = fmaf(x[r][e], q[e], o[r]);
+      }
+      if constexpr (kPer == 4)
+        __stcs(reinterpret_cast<float4*>(Sm + (r0 + r) * D) + lane, make_float4(x[r][0], x[r][1], x[r][2], x[r][3]));
+      else
+        __stcs(reinterpret_cast<float2*>(Sm + (r0 + r) * D) + lane, make_float2(x[r][0], x[r][1]));
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) o[r] += __shfl_xor_sync(0xffffffffu, o[r], m);
+    if (lane < kRows) {
+      float y = o[0];
+#pragma unroll
+      for (int r = 1; r < kRows; ++r) y = lane == r ? o[r] : y;
+      Or[r0 + lane] = __float2bfloat16_rn(c.scale * y);
+    }
+  }
+}
+
+constexpr int kMinSegChunks = 8;
+
+// Chunks per segment. A sequence longer than half of one SM's share of the whole
+// work is cut, but not into less than kMinSegChunks (a segment reads its keys
+// and values twice, and starts from a state).
+int segment_chunks(const vda_decay_config& c, int njobs) {
+  const long long chunks = ((long long)c.T + kC - 1) / kC + c.N / 2;
+  const long long share = chunks * c.H * njobs / 148;
+  return (int)std::min<long long>(1 << 20, std::max<long long>(kMinSegChunks, (share + 1) / 2));
+}
+long long segment_items(const vda_decay_config& c, int seg) { return (long long)c.T / ((long long)seg * kC) + c.N; }
+
+template <int D>
+cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr[4], const long long row[4], int nmaps,
+                     void* ws, cudaStream_t s) {
+  using C = DaCfg<D>;
+  a.seg = segment_chunks(c, a.njobs);
+  const bool whole = (long long)c.T <= (long long)a.seg * kC;  // no sequence can be longer than a segment
+  const long long items = segment_items(c, a.seg);
+  a.seg_state = whole ? nullptr : static_cast<float*>(ws);
+  a.wait_ns = 2000000000ull;
+  const long long grid = items * c.H * a.njobs;
+  if (grid >= (1LL << 31) || c.N > 65535) return cudaErrorInvalidConfiguration;
+  DaMaps maps{};
+  cudaError_t e;
+  uint64_t dims[3] = {(uint64_t)D, (uint64_t)c.H, (uint64_t)std::max(1, c.T)};
+  uint32_t box[3] = {64, 1, (uint32_t)kC};
+  for (int i = 0; i < nmaps; ++i) {
+    uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)row[i] * 2};
+    if ((e = make_tmap_bf16(&maps.m[i], ptr[i], 3, dims, str, box)) != cudaSuccess) return e;
+  }
+  const void* main_fn = reinterpret_cast<const void*>(decay_attn_tc_kernel<D, false>);
+  const void* state_fn = reinterpret_cast<const void*>(decay_attn_tc_kernel<D, true>);
+  if ((e = set_max_dynamic_smem(main_fn, C::kSmemBytes)) != cudaSuccess) return e;
+  if ((e = set_max_dynamic_smem(state_fn, C::kSmemBytes)) != cudaSuccess) return e;
+  if (!whole) {
+    decay_attn_tc_kernel<D, true><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(maps, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const dim3 jg((unsigned)(c.H * a.njobs * (D * D / 1024)), (unsigned)c.N);
+    decay_join_kernel<D><<<jg, 256, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  decay_attn_tc_kernel<D, false><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(maps, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decay_attention_workspace(const vda_decay_config& c, bool backward) {
+  const int njobs = backward ? 3 : 1;
+  const int seg = segment_chunks(c, njobs);
+  if ((long long)c.T <= (long long)seg * kC) return 0;
+  return (size_t)segment_items(c, seg) * c.H * njobs * c.d * c.d * sizeof(float);
+}
+
+cudaError_t launch_decay_attention(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                                   const float* log_decay, const int* cu, const float* S0, void* O, float* S_last,
+                                   void* ws, uint32_t* status, cudaStream_t s) {
+  DaArgs a{};
+  a.N = c.N; a.H = c.H; a.T = c.T; a.njobs = 1;
+  a.cu = cu;
+  a.log_decay = log_decay;
+  a.status = status;
+  a.job[0] = DaJob{0, 1, 2, 0, 0, c.scale, c.scale, 1.f, S0, S_last, static_cast<__nv_bfloat16*>(O), c.o_row};
+  const void* ptr[4] = {Q, K, V, nullptr};
+  const long long row[4] = {c.q_row, c.k_row, c.v_row, 0};
+  return c.d == 128 ? launch_d<128>(c, a, ptr, row, 3, ws, s) : launch_d<64>(c, a, ptr, row, 3, ws, s);
+}
+
+cudaError_t launch_decay_attention_backward(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                                            const void* dO, const float* log_decay, const int* cu, const float* S0,
+                                            const float* dS, void* dQ, void* dK, void* dV, float* dS0, void* ws,
+                                            uint32_t* status, cudaStream_t s) {
+  DaArgs a{};
+  a.N = c.N; a.H = c.H; a.T = c.T; a.njobs = 3;
+  a.cu = cu;
+  a.log_decay = log_decay;
+  a.status = status;
+  const long long g_row = (long long)c.H * c.d;  // gradients are packed without gaps
+  // Maps: 0 Q, 1 K, 2 V, 3 dO.
+  a.job[0] = DaJob{3, 2, 1, 0, 1, c.scale, c.scale, 1.f, S0, nullptr, static_cast<__nv_bfloat16*>(dQ), g_row};
+  a.job[1] = DaJob{2, 3, 0, 1, 1, c.scale, 1.f, c.scale, dS, nullptr, static_cast<__nv_bfloat16*>(dK), g_row};
+  a.job[2] = DaJob{1, 0, 3, 1, 0, c.scale, 1.f, c.scale, dS, dS0, static_cast<__nv_bfloat16*>(dV), g_row};
+  const void* ptr[4] = {Q, K, V, dO};
+  const long long row[4] = {c.q_row, c.k_row, c.v_row, c.o_row};
+  return c.d == 128 ? launch_d<128>(c, a, ptr, row, 4, ws, s) : launch_d<64>(c, a, ptr, row, 4, ws, s);
+}
+
+cudaError_t launch_decay_step(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                              const float* log_decay, float* S, void* O, cudaStream_t s) {
+  // Enough CTAs for every SM: a matrix is shared by up to D / 32 of them.
+  int slabs = 1;
+  while (slabs < c.d / 32 && (long long)c.N * c.H * slabs < 148 * 4) slabs *= 2;
+  const long long grid = (long long)c.N * c.H * slabs;
+  if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+  const auto* q = static_cast<const __nv_bfloat16*>(Q);
+  const auto* k = static_cast<const __nv_bfloat16*>(K);
+  const auto* v = static_cast<const __nv_bfloat16*>(V);
+  auto* o = static_cast<__nv_bfloat16*>(O);
+  if (c.d == 128)
+    decay_step_kernel<128><<<(unsigned)grid, 256, 0, s>>>(c, q, k, v, log_decay, S, o, slabs);
+  else
+    decay_step_kernel<64><<<(unsigned)grid, 256, 0, s>>>(c, q, k, v, log_decay, S, o, slabs);
+  return cudaGetLastError();
+}
+
+}  // namespace vda

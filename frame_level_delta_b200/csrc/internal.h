@@ -202,4 +202,25 @@ cudaError_t launch_gram_fp8_tc(const Problem& p, const void* K8, const void* V8,
 cudaError_t launch_merge_tc(const void* A1, const void* B1, const void* A2, const void* B2, void* Y, int M, int N,
                             int K1, int K2, uint32_t* status, unsigned long long wait_ns, cudaStream_t s);
 
+// The prompt path (packed sequences; see the declarations in vda.h).
+size_t causal_attention_workspace(const vda_attention_config& c);
+cudaError_t launch_causal_attention(const vda_attention_config& c, const void* Q, const void* K, const void* V,
+                                    const int* cu_q, const int* cu_k, const int* k_len, void* O, float* lse, void* ws,
+                                    uint32_t* status, cudaStream_t s);
+size_t causal_attention_backward_workspace(const vda_attention_config& c);
+cudaError_t launch_causal_attention_backward(const vda_attention_config& c, const void* Q, const void* K,
+                                             const void* V, const void* O, const void* dO, const float* lse,
+                                             const int* cu_q, const int* cu_k, const int* k_len, void* dQ, void* dK,
+                                             void* dV, void* ws, uint32_t* status, cudaStream_t s);
+size_t decay_attention_workspace(const vda_decay_config& c, bool backward);
+cudaError_t launch_decay_attention(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                                   const float* log_decay, const int* cu, const float* S0, void* O, float* S_last,
+                                   void* ws, uint32_t* status, cudaStream_t s);
+cudaError_t launch_decay_attention_backward(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                                            const void* dO, const float* log_decay, const int* cu, const float* S0,
+                                            const float* dS, void* dQ, void* dK, void* dV, float* dS0, void* ws,
+                                            uint32_t* status, cudaStream_t s);
+cudaError_t launch_decay_step(const vda_decay_config& c, const void* Q, const void* K, const void* V,
+                              const float* log_decay, float* S, void* O, cudaStream_t s);
+
 }  // namespace vda

@@ -1,0 +1,102 @@
+// Packed sequences: what the kernels of the prompt path share. Sequence i of a
+// packed tensor holds tokens cu[i] .. cu[i+1]-1. The prefix array is device data
+// that the host never reads, so every bound taken from it is clamped to the
+// tensor: a wrong array gives wrong rows, never an access out of range.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sm100.cuh"
+
+namespace vda {
+namespace seq {
+
+// [lo, hi) of sequence i, clamped to a tensor of T tokens.
+__device__ __forceinline__ void bounds(const int* cu, int i, int T, int& lo, int& hi) {
+  lo = min(max(__ldg(cu + i), 0), T);
+  hi = min(max(__ldg(cu + i + 1), lo), T);
+}
+
+// Work item x of a list in which sequence i has count(i) items: returns the
+// sequence and x's index within it, or -1 past the list's end. Every thread of
+// the block calls it; `scratch` holds 40 ints. Each pass takes blockDim.x
+// sequences (one load and one scan), so up to that many cost one pass.
+template <typename Count>
+__device__ __forceinline__ int find_item(int x, int N, int* scratch, Count count, int& idx) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (threadIdx.x == 0) scratch[33] = -1;
+  for (int base = 0; base < N; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    const int c = i < N ? count(i) : 0;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int off = 0, total = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int t = scratch[w];
+      if (w < warp) off += t;
+      total += t;
+    }
+    const int hi = off + inc, lo = hi - c;
+    if (x >= lo && x < hi) {
+      scratch[33] = i;
+      scratch[34] = x - lo;
+    }
+    __syncthreads();
+    if (scratch[33] >= 0) break;
+    x -= total;
+  }
+  __syncthreads();
+  idx = scratch[34];
+  return scratch[33];
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return sm100::bf162_bits(__floats2bfloat162_rn(a, b));
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// Zeroes 16-byte chunk c (of 8) of token row `row` in each of `atoms` boxes of
+// 128 token rows x 64 channels (128-byte rows; a whole row is zeroed, so the
+// swizzle does not matter). For rows past a sequence's end: they hold another
+// sequence's values or whatever lies behind the last one, and 0 x NaN is NaN.
+__device__ __forceinline__ void zero_row(uint8_t* tile, int atoms, int row, int rows_per_atom) {
+  for (int at = 0; at < atoms; ++at) {
+    uint4* p = reinterpret_cast<uint4*>(tile + (size_t)at * rows_per_atom * 128 + row * 128);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) p[c] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+}  // namespace seq
+
+// One 32-bit status word per device, owned by the library: zero until a bounded
+// device-side wait of a packed-sequence kernel gives up (then VDA_ERR_TIMEOUT),
+// cleared by vda_sequence_poll. Returns the current device's address of it.
+cudaError_t sequence_status(uint32_t** word);
+
+}  // namespace vda

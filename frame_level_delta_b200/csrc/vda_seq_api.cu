@@ -1,0 +1,240 @@
+// Host side of the prompt path's calls (packed sequences): argument checks and
+// the per-device status word. Every call only enqueues work.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <initializer_list>
+#include <mutex>
+
+#include "internal.h"
+#include "seq.cuh"
+
+namespace vda {
+
+namespace {
+
+__device__ __align__(256) uint32_t g_sequence_status[64];
+
+constexpr int kMaxDevices = 64;
+std::atomic<void*> g_status_addr[kMaxDevices];
+std::mutex g_status_mu;
+
+}  // namespace
+
+// The current device's address of the word, asked of the runtime once per device.
+cudaError_t sequence_status(uint32_t** word) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  void* p = g_status_addr[dev].load(std::memory_order_acquire);
+  if (p == nullptr) {
+    std::lock_guard<std::mutex> lock(g_status_mu);
+    p = g_status_addr[dev].load(std::memory_order_relaxed);
+    if (p == nullptr) {
+      if ((e = cudaGetSymbolAddress(&p, g_sequence_status)) != cudaSuccess) return e;
+      g_status_addr[dev].store(p, std::memory_order_release);
+    }
+  }
+  *word = static_cast<uint32_t*>(p);
+  return cudaSuccess;
+}
+
+}  // namespace vda
+
+using namespace vda;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool any_null(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p) return true;
+  return false;
+}
+bool all_aligned(std::initializer_list<const void*> ps, uintptr_t n) {
+  for (const void* p : ps)
+    if (p && !aligned(p, n)) return false;
+  return true;
+}
+// Rows of `width` elements, `row` apart. 2^37 elements between rows is what a
+// tensor map's stride field holds.
+bool good_row(long long row, long long width) { return row >= width && row % 8 == 0 && row < (1LL << 37); }
+
+vda_status check(const vda_attention_config* c) {
+  if (!c || c->N < 1 || c->Hq < 1 || c->Hkv < 1 || c->Tq < 0 || c->Tk < 0) return VDA_ERR_INVALID_ARG;
+  if (c->Hq % c->Hkv != 0) return VDA_ERR_INVALID_ARG;
+  if (!(c->scale > 0.f) || !std::isfinite(c->scale)) return VDA_ERR_INVALID_ARG;
+  if ((c->d != 64 && c->d != 128) || c->Hq / c->Hkv > 128) return VDA_ERR_UNSUPPORTED;
+  const long long wq = (long long)c->Hq * c->d, wk = (long long)c->Hkv * c->d;
+  if (!good_row(c->q_row, wq) || !good_row(c->o_row, wq) || !good_row(c->k_row, wk) || !good_row(c->v_row, wk))
+    return VDA_ERR_INVALID_ARG;
+  // The tile lists are 32-bit: N + Tq, Tk stay below 2^30.
+  if (c->N >= (1 << 30) || c->Tq >= (1 << 30) || c->Tk >= (1 << 30)) return VDA_ERR_UNSUPPORTED;
+  return VDA_OK;
+}
+
+vda_status check(const vda_decay_config* c) {
+  if (!c || c->N < 1 || c->H < 1 || c->T < 0 || !std::isfinite(c->scale)) return VDA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return VDA_ERR_UNSUPPORTED;
+  const long long w = (long long)c->H * c->d;
+  if (!good_row(c->q_row, w) || !good_row(c->k_row, w) || !good_row(c->v_row, w) || !good_row(c->o_row, w))
+    return VDA_ERR_INVALID_ARG;
+  if (c->T >= (1 << 30)) return VDA_ERR_UNSUPPORTED;
+  return VDA_OK;
+}
+// The prompt kernels run sequences on grid.y of one of their launches.
+vda_status check_prompt(const vda_decay_config* c) {
+  vda_status st = check(c);
+  return st != VDA_OK ? st : c->N > 65535 ? VDA_ERR_UNSUPPORTED : VDA_OK;
+}
+
+vda_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return VDA_OK;
+  if (!ws) return VDA_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return VDA_ERR_ALIGNMENT;
+  return have < need ? VDA_ERR_WORKSPACE_TOO_SMALL : VDA_OK;
+}
+
+vda_status of(cudaError_t e) {
+  return e == cudaSuccess ? VDA_OK : e == cudaErrorInvalidConfiguration ? VDA_ERR_UNSUPPORTED : VDA_ERR_CUDA;
+}
+
+// What becomes of states when there is no token at all: the state stays.
+cudaError_t keep_state(const vda_decay_config& c, const float* from, float* to, cudaStream_t s) {
+  if (!to || to == from) return cudaSuccess;
+  const size_t bytes = (size_t)c.N * c.H * c.d * c.d * sizeof(float);
+  return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+vda_status vda_causal_attention_workspace(const vda_attention_config* cfg, size_t* bytes) {
+  if (!bytes) return VDA_ERR_INVALID_ARG;
+  vda_status st = check(cfg);
+  if (st == VDA_OK) *bytes = causal_attention_workspace(*cfg);
+  return st;
+}
+
+vda_status vda_causal_attention(const vda_attention_config* cfg, const void* Q, const void* K, const void* V,
+                                const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* O, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  vda_status st = check(cfg);
+  if (st != VDA_OK) return st;
+  if (any_null({cu_q, cu_k}) || (cfg->Tq > 0 && any_null({Q, O})) || (cfg->Tk > 0 && any_null({K, V})))
+    return VDA_ERR_INVALID_ARG;
+  if (!all_aligned({Q, K, V, O}, 16) || !all_aligned({cu_q, cu_k, k_len, lse}, 4)) return VDA_ERR_ALIGNMENT;
+  if ((st = check_ws(workspace, workspace_bytes, causal_attention_workspace(*cfg))) != VDA_OK) return st;
+  if (cfg->Tq == 0) return VDA_OK;
+  uint32_t* status = nullptr;
+  cudaError_t e = sequence_status(&status);
+  if (e == cudaSuccess)
+    e = launch_causal_attention(*cfg, Q, K, V, cu_q, cu_k, k_len, O, lse, workspace, status,
+                                static_cast<cudaStream_t>(stream));
+  return of(e);
+}
+
+vda_status vda_causal_attention_backward_workspace(const vda_attention_config* cfg, size_t* bytes) {
+  if (!bytes) return VDA_ERR_INVALID_ARG;
+  vda_status st = check(cfg);
+  if (st == VDA_OK) *bytes = causal_attention_backward_workspace(*cfg);
+  return st;
+}
+
+vda_status vda_causal_attention_backward(const vda_attention_config* cfg, const void* Q, const void* K,
+                                         const void* V, const void* O, const void* dO, const float* lse,
+                                         const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* dQ,
+                                         void* dK, void* dV, void* workspace, size_t workspace_bytes, void* stream) {
+  vda_status st = check(cfg);
+  if (st != VDA_OK) return st;
+  if (any_null({cu_q, cu_k}) || (cfg->Tq > 0 && any_null({Q, O, dO, lse, dQ})) ||
+      (cfg->Tk > 0 && any_null({K, V, dK, dV})))
+    return VDA_ERR_INVALID_ARG;
+  if (!all_aligned({Q, K, V, O, dO, dQ, dK, dV}, 16) || !all_aligned({cu_q, cu_k, k_len, lse}, 4))
+    return VDA_ERR_ALIGNMENT;
+  if ((st = check_ws(workspace, workspace_bytes, causal_attention_backward_workspace(*cfg))) != VDA_OK) return st;
+  if (cfg->Tq == 0 && cfg->Tk == 0) return VDA_OK;
+  uint32_t* status = nullptr;
+  cudaError_t e = sequence_status(&status);
+  if (e == cudaSuccess)
+    e = launch_causal_attention_backward(*cfg, Q, K, V, O, dO, lse, cu_q, cu_k, k_len, dQ, dK, dV, workspace, status,
+                                         static_cast<cudaStream_t>(stream));
+  return of(e);
+}
+
+vda_status vda_decay_attention_workspace(const vda_decay_config* cfg, size_t* bytes) {
+  if (!bytes) return VDA_ERR_INVALID_ARG;
+  vda_status st = check_prompt(cfg);
+  if (st == VDA_OK) *bytes = decay_attention_workspace(*cfg, false);
+  return st;
+}
+
+vda_status vda_decay_attention(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const int32_t* cu, const float* S0, void* O, float* S,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  vda_status st = check_prompt(cfg);
+  if (st != VDA_OK) return st;
+  if (any_null({log_decay, cu}) || (cfg->T > 0 && any_null({Q, K, V, O}))) return VDA_ERR_INVALID_ARG;
+  if (!all_aligned({Q, K, V, O, S0, S}, 16) || !all_aligned({log_decay, cu}, 4)) return VDA_ERR_ALIGNMENT;
+  if ((st = check_ws(workspace, workspace_bytes, decay_attention_workspace(*cfg, false))) != VDA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cfg->T == 0) return of(keep_state(*cfg, S0, S, s));
+  uint32_t* status = nullptr;
+  cudaError_t e = sequence_status(&status);
+  if (e == cudaSuccess) e = launch_decay_attention(*cfg, Q, K, V, log_decay, cu, S0, O, S, workspace, status, s);
+  return of(e);
+}
+
+vda_status vda_decay_attention_step(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                                    const float* log_decay, float* S, void* O, void* stream) {
+  vda_status st = check(cfg);
+  if (st != VDA_OK) return st;
+  if (cfg->T != cfg->N || any_null({Q, K, V, log_decay, S, O})) return VDA_ERR_INVALID_ARG;
+  if (!all_aligned({Q, K, V, O, S}, 16) || !all_aligned({log_decay}, 4)) return VDA_ERR_ALIGNMENT;
+  return of(launch_decay_step(*cfg, Q, K, V, log_decay, S, O, static_cast<cudaStream_t>(stream)));
+}
+
+vda_status vda_decay_attention_backward_workspace(const vda_decay_config* cfg, size_t* bytes) {
+  if (!bytes) return VDA_ERR_INVALID_ARG;
+  vda_status st = check_prompt(cfg);
+  if (st == VDA_OK) *bytes = decay_attention_workspace(*cfg, true);
+  return st;
+}
+
+vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                                        const void* dO, const float* log_decay, const int32_t* cu, const float* S0,
+                                        const float* dS, void* dQ, void* dK, void* dV, float* dS0, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  vda_status st = check_prompt(cfg);
+  if (st != VDA_OK) return st;
+  if (any_null({log_decay, cu}) || (cfg->T > 0 && any_null({Q, K, V, dO, dQ, dK, dV}))) return VDA_ERR_INVALID_ARG;
+  if (dS0 && (dS0 == dS || dS0 == S0)) return VDA_ERR_INVALID_ARG;
+  if (!all_aligned({Q, K, V, dO, dQ, dK, dV, S0, dS, dS0}, 16) || !all_aligned({log_decay, cu}, 4))
+    return VDA_ERR_ALIGNMENT;
+  if ((st = check_ws(workspace, workspace_bytes, decay_attention_workspace(*cfg, true))) != VDA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cfg->T == 0) return of(keep_state(*cfg, dS, dS0, s));
+  uint32_t* status = nullptr;
+  cudaError_t e = sequence_status(&status);
+  if (e == cudaSuccess)
+    e = launch_decay_attention_backward(*cfg, Q, K, V, dO, log_decay, cu, S0, dS, dQ, dK, dV, dS0, workspace, status,
+                                        s);
+  return of(e);
+}
+
+vda_status vda_sequence_poll(void* stream) {
+  uint32_t* word = nullptr;
+  if (sequence_status(&word) != cudaSuccess) return VDA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return VDA_ERR_CUDA;
+  if (v == 0) return VDA_OK;
+  return cudaMemsetAsync(word, 0, sizeof(v), s) == cudaSuccess ? VDA_ERR_TIMEOUT : VDA_ERR_CUDA;
+}
+
+}  // extern "C"

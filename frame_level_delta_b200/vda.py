@@ -39,7 +39,11 @@ EXPORTS = ["vda_create", "vda_destroy", "vda_workspace_size", "vda_prepare", "vd
            "vda_last_error", "vda_profile_enable", "vda_num_kernels", "vda_profile_read",
            "vda_launch_count", "vda_describe", "vda_selftest_bounded_wait",
            "vda_selftest_recip", "vda_static_workspace_capacity", "vda_run_static_workspace",
-           "vda_static_workspace_poll"]
+           "vda_static_workspace_poll",
+           "vda_causal_attention_workspace", "vda_causal_attention", "vda_causal_attention_backward_workspace",
+           "vda_causal_attention_backward", "vda_decay_attention_workspace", "vda_decay_attention",
+           "vda_decay_attention_step", "vda_decay_attention_backward_workspace", "vda_decay_attention_backward",
+           "vda_sequence_poll"]
 
 
 class VDAError(RuntimeError):
@@ -54,6 +58,19 @@ class vda_config(ctypes.Structure):
                 ("d_k", ctypes.c_int), ("d_v", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("flags", ctypes.c_uint), ("l2_eps", ctypes.c_float),
                 ("rms_eps", ctypes.c_float), ("H_total", ctypes.c_int), ("h0", ctypes.c_int)]
+
+
+class vda_attention_config(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("Tq", ctypes.c_int), ("Tk", ctypes.c_int), ("q_row", ctypes.c_longlong),
+                ("k_row", ctypes.c_longlong), ("v_row", ctypes.c_longlong), ("o_row", ctypes.c_longlong),
+                ("scale", ctypes.c_float)]
+
+
+class vda_decay_config(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int), ("T", ctypes.c_int),
+                ("q_row", ctypes.c_longlong), ("k_row", ctypes.c_longlong), ("v_row", ctypes.c_longlong),
+                ("o_row", ctypes.c_longlong), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -98,6 +115,18 @@ def lib() -> ctypes.CDLL:
         L.vda_static_workspace_capacity.argtypes = []
         L.vda_static_workspace_capacity.restype = ctypes.c_size_t
         L.vda_run_static_workspace.argtypes = [cfgp] + [vp] * 11 + [vp]
+        szp = ctypes.POINTER(sz)
+        acfg, dcfg = ctypes.POINTER(vda_attention_config), ctypes.POINTER(vda_decay_config)
+        L.vda_causal_attention_workspace.argtypes = [acfg, szp]
+        L.vda_causal_attention.argtypes = [acfg] + [vp] * 9 + [sz, vp]
+        L.vda_causal_attention_backward_workspace.argtypes = [acfg, szp]
+        L.vda_causal_attention_backward.argtypes = [acfg] + [vp] * 13 + [sz, vp]
+        L.vda_decay_attention_workspace.argtypes = [dcfg, szp]
+        L.vda_decay_attention.argtypes = [dcfg] + [vp] * 9 + [sz, vp]
+        L.vda_decay_attention_step.argtypes = [dcfg] + [vp] * 7
+        L.vda_decay_attention_backward_workspace.argtypes = [dcfg, szp]
+        L.vda_decay_attention_backward.argtypes = [dcfg] + [vp] * 13 + [sz, vp]
+        L.vda_sequence_poll.argtypes = [vp]
         for name in EXPORTS:
             if name not in ("vda_status_string", "vda_last_error", "vda_static_workspace_capacity"):
                 getattr(L, name).restype = ctypes.c_int
@@ -522,6 +551,273 @@ def selftest_recip(x: torch.Tensor, stream=None) -> torch.Tensor:
 
 def selftest_bounded_wait(status: torch.Tensor, spins: int, stream=None) -> int:
     return lib().vda_selftest_bounded_wait(_ptr(status), spins, _stream_handle(stream))
+
+
+# ---------------------------------------------------------------- the prompt path
+# Packed sequences: cu is the int32 device tensor [N + 1] of sequence starts, and
+# tokens cu[i] .. cu[i+1]-1 are sequence i's. Token tensors are [tokens, heads, d]
+# bf16 with contiguous heads and any distance between tokens (a slice of the
+# heads, a part of a joint projection); outputs made here are contiguous, and
+# their rows outside the sequences stay uninitialised.
+
+
+def _rows(name: str, t, shape: tuple, dev) -> int:
+    """Check a token tensor (``shape`` may hold None for a free extent); its row distance in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected torch.bfloat16")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}; this call runs on {dev}")
+    s = t.shape
+    if len(s) != 3 or any(w is not None and w != g for w, g in zip(shape, s)):
+        raise ValueError(f"{name} has shape {tuple(s)}; expected {tuple('any' if w is None else w for w in shape)}")
+    row, head, one = t.stride()
+    d = s[2]
+    if (one != 1 and d > 1) or (head != d and s[1] > 1):
+        raise ValueError(f"{name} must have contiguous heads (strides (any, {d}, 1), not {t.stride()})")
+    if s[0] < 2:  # a distance that no access uses
+        return s[1] * d
+    if row % 8 or row < s[1] * d:
+        raise ValueError(f"{name}: tokens must lie a multiple of 8 elements apart and not overlap (got {row})")
+    return row
+
+
+def _flat(name: str, t, shape: tuple, dtype, dev):
+    """Check a contiguous tensor of known shape (None: not given)."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}; this call runs on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _starts(name: str, cu, dev) -> int:
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError(f"{name} must be an int32 tensor of sequence starts, [N + 1]")
+    _flat(name, cu, tuple(cu.shape), torch.int32, dev)
+    return cu.shape[0] - 1
+
+
+def _cuda_device(t) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"Q: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"the library runs on CUDA devices; Q is on {t.device}")
+    return t.device
+
+
+class _On:
+    """The device and stream of a call: what is allocated inside belongs to the stream it is used on."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self.guard = None
+        if self.stream is not None:
+            if self.stream.device != self.dev:
+                raise ValueError(f"the stream is on {self.stream.device}; the tensors are on {self.dev}")
+            self.guard = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+        if self.guard is not None:
+            self.guard.__enter__()
+        return ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _workspace(what: str, cfg, dev) -> Tuple[Optional[torch.Tensor], int]:
+    n = ctypes.c_size_t(0)
+    st = getattr(lib(), what)(ctypes.byref(cfg), ctypes.byref(n))
+    if st != VDA_OK:
+        raise VDAError(st, what)
+    if n.value == 0:
+        return None, 0
+    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+
+
+def _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev) -> vda_attention_config:
+    N = _starts("cu_q", cu_q, dev)
+    if cu_k is not cu_q and _starts("cu_k", cu_k, dev) != N:
+        raise ValueError("cu_q and cu_k hold different numbers of sequences")
+    _flat("k_len", k_len, (N,), torch.int32, dev)
+    q_row = _rows("Q", Q, (None, None, None), dev)
+    Tq, Hq, d = Q.shape
+    k_row = _rows("K", K, (None, None, d), dev)
+    Tk, Hkv, _ = K.shape
+    v_row = _rows("V", V, (Tk, Hkv, d), dev)
+    o_row = Hq * d if O is None else _rows("O", O, (Tq, Hq, d), dev)
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads are no multiple of {Hkv} key heads")
+    if cu_k is cu_q and Tk != Tq:
+        raise ValueError(f"K has {Tk} tokens and Q {Tq}: give cu_k where keys and queries are not the same tokens")
+    return vda_attention_config(N, Hq, Hkv, d, Tq, Tk, q_row, k_row, v_row, o_row,
+                                d ** -0.5 if scale is None else scale)
+
+
+def causal_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
+                     cu_k: Optional[torch.Tensor] = None, k_len: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, O: Optional[torch.Tensor] = None, return_lse: bool = False,
+                     stream=None):
+    """Causal softmax attention over packed sequences with grouped heads
+    (vda_causal_attention): Q [Tq, Hq, d], K, V [Tk, Hkv, d] bf16, d 64 or 128.
+    The last query of a sequence stands at its last key, so one query per sequence
+    against a cache (cu_k: the caches' rooms, k_len: their filled parts) is a step
+    of generation. ``scale`` defaults to 1 / sqrt(d). Returns O, or (O, lse) with
+    lse [Tq, Hq] float32."""
+    dev = _cuda_device(Q)
+    if cu_k is None:
+        cu_k = cu_q
+    c = _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev)
+    with _On(dev, stream) as s:
+        ws, n = _workspace("vda_causal_attention_workspace", c, dev)
+        if O is None:
+            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+        st = lib().vda_causal_attention(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(cu_q), _ptr(cu_k),
+                                        _ptr(k_len), _ptr(O), _ptr(lse), _ptr(ws), n, s)
+    if st != VDA_OK:
+        raise VDAError(st, "vda_causal_attention")
+    return (O, lse) if return_lse else O
+
+
+def causal_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+                              dO: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor,
+                              cu_k: Optional[torch.Tensor] = None, k_len: Optional[torch.Tensor] = None,
+                              scale: Optional[float] = None, out: Optional[Dict[str, torch.Tensor]] = None,
+                              stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of causal_attention (vda_causal_attention_backward) from the O and
+    lse it returned: dQ, dK, dV (bf16, contiguous). Rows outside the sequences are
+    not written: uninitialised in tensors made here, as they were in ``out``."""
+    dev = _cuda_device(Q)
+    if cu_k is None:
+        cu_k = cu_q
+    c = _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev)
+    if _rows("dO", dO, tuple(O.shape), dev) != c.o_row and O.shape[0] > 1:
+        raise ValueError("O and dO must have the same distance between tokens")
+    _flat("lse", lse, tuple(Q.shape[:2]), torch.float32, dev)
+    with _On(dev, stream) as s:
+        ws, n = _workspace("vda_causal_attention_backward_workspace", c, dev)
+        if out is None:
+            out = {k: torch.empty(t.shape, dtype=t.dtype, device=dev) for k, t in (("dQ", Q), ("dK", K), ("dV", V))}
+        for k, t in (("dQ", Q), ("dK", K), ("dV", V)):
+            _flat(k, out[k], tuple(t.shape), torch.bfloat16, dev)
+        st = lib().vda_causal_attention_backward(
+            ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
+            _ptr(k_len), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(ws), n, s)
+    if st != VDA_OK:
+        raise VDAError(st, "vda_causal_attention_backward")
+    return out
+
+
+def _decay_config(Q, K, V, O, log_decay, N, scale, dev, oname="O") -> vda_decay_config:
+    q_row = _rows("Q", Q, (None, None, None), dev)
+    T, H, d = Q.shape
+    k_row, v_row = _rows("K", K, (T, H, d), dev), _rows("V", V, (T, H, d), dev)
+    o_row = H * d if O is None else _rows(oname, O, (T, H, d), dev)
+    _flat("log_decay", log_decay, (H,), torch.float32, dev)
+    return vda_decay_config(N, H, d, T, q_row, k_row, v_row, o_row, scale)
+
+
+def decay_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay: torch.Tensor, cu: torch.Tensor,
+                    S0: Optional[torch.Tensor] = None, scale: float = 1.0, O: Optional[torch.Tensor] = None,
+                    S: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Linear attention with a decay for each head over packed sequences
+    (vda_decay_attention): S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T,
+    o_t = scale S_t q_t. Q, K, V [T, H, d] bf16, d 64 or 128; log_decay [H]
+    float32; S0 [N, H, d, d] float32, zero if not given. Returns O and the states
+    after each sequence (``S`` may be S0: updated in place)."""
+    dev = _cuda_device(Q)
+    N = _starts("cu", cu, dev)
+    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
+    shape = (N, c.H, c.d, c.d)
+    _flat("S0", S0, shape, torch.float32, dev)
+    _flat("S", S, shape, torch.float32, dev)
+    with _On(dev, stream) as s:
+        ws, n = _workspace("vda_decay_attention_workspace", c, dev)
+        if O is None:
+            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        if S is None:
+            S = torch.empty(shape, dtype=torch.float32, device=dev)
+        st = lib().vda_decay_attention(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(log_decay), _ptr(cu),
+                                       _ptr(S0), _ptr(O), _ptr(S), _ptr(ws), n, s)
+    if st != VDA_OK:
+        raise VDAError(st, "vda_decay_attention")
+    return O, S
+
+
+def decay_attention_step(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay: torch.Tensor,
+                         S: torch.Tensor, scale: float = 1.0, O: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """One token of every sequence through decay_attention's recurrence
+    (vda_decay_attention_step): row n of Q, K, V [N, H, d] belongs to state S[n],
+    which is updated in place. Returns O [N, H, d]."""
+    dev = _cuda_device(Q)
+    N = Q.shape[0]
+    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
+    _flat("S", S, (N, c.H, c.d, c.d), torch.float32, dev)
+    if S is None:
+        raise ValueError("S is required")
+    with _On(dev, stream) as s:
+        if O is None:
+            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        if N == 0:
+            return O
+        st = lib().vda_decay_attention_step(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(log_decay), _ptr(S),
+                                            _ptr(O), s)
+    if st != VDA_OK:
+        raise VDAError(st, "vda_decay_attention_step")
+    return O
+
+
+def decay_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
+                             log_decay: torch.Tensor, cu: torch.Tensor, S0: Optional[torch.Tensor] = None,
+                             dS: Optional[torch.Tensor] = None, scale: float = 1.0,
+                             out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of decay_attention (vda_decay_attention_backward) for dL/dO and,
+    where given, dL/dS of the last states: dQ, dK, dV (bf16, contiguous) and dS0
+    (float32). Rows outside the sequences are not written: uninitialised in
+    tensors made here, as they were in ``out``."""
+    dev = _cuda_device(Q)
+    N = _starts("cu", cu, dev)
+    if dO is None:
+        raise ValueError("dO is required")
+    c = _decay_config(Q, K, V, dO, log_decay, N, scale, dev, "dO")
+    shape = (N, c.H, c.d, c.d)
+    _flat("S0", S0, shape, torch.float32, dev)
+    _flat("dS", dS, shape, torch.float32, dev)
+    with _On(dev, stream) as s:
+        ws, n = _workspace("vda_decay_attention_backward_workspace", c, dev)
+        if out is None:
+            out = {k: torch.empty(Q.shape, dtype=Q.dtype, device=dev) for k in ("dQ", "dK", "dV")}
+            out["dS0"] = torch.empty(shape, dtype=torch.float32, device=dev)
+        for k in ("dQ", "dK", "dV"):
+            _flat(k, out[k], tuple(Q.shape), torch.bfloat16, dev)
+        _flat("dS0", out.get("dS0"), shape, torch.float32, dev)
+        st = lib().vda_decay_attention_backward(
+            ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(log_decay), _ptr(cu), _ptr(S0), _ptr(dS),
+            _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out.get("dS0")), _ptr(ws), n, s)
+    if st != VDA_OK:
+        raise VDAError(st, "vda_decay_attention_backward")
+    return out
+
+
+def sequence_poll(stream=None) -> int:
+    """Status of the prompt path's calls on the current device since the last poll
+    (synchronises the stream; VDA_ERR_TIMEOUT if a device-side wait gave up)."""
+    return lib().vda_sequence_poll(_stream_handle(stream))
 
 
 def to_device(inp: Dict[str, torch.Tensor], device="cuda") -> Dict[str, torch.Tensor]:

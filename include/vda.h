@@ -418,6 +418,135 @@ vda_status vda_run_static_workspace(const vda_config* cfg, const void* Q, const 
  */
 vda_status vda_static_workspace_poll(void* stream);
 
+/*
+ * The prompt path: attention over tokens that come one after another (the text
+ * that conditions a clip, or tokens generated one by one), beside the frame
+ * geometry of the calls above. Sequences are packed: sequence i of a packed
+ * tensor is tokens cu[i] .. cu[i+1]-1, cu being N + 1 int32 values in device
+ * memory, not decreasing, within 0 .. the tensor's tokens. The host never reads
+ * them; values out of that range are clamped to it (wrong rows, no access out of
+ * range). Rows of tokens outside cu[0] .. cu[N]-1 are never read into a result
+ * and never written. Within a sequence the values are expected to be finite.
+ *
+ * Token tensors hold one row per token, [heads, d] contiguous within it; the
+ * distance between rows is given in elements (q_row, ...), so that a slice of
+ * the heads, or a part of a joint projection, is passed as it lies. Rows are a
+ * multiple of 8 elements apart and at least heads * d; pointers are 16-byte
+ * aligned. bf16 storage, d 64 or 128, every sum and state in fp32.
+ *
+ * These calls take no context and keep no device memory. They only enqueue work;
+ * all argument errors come back before any launch. Calls that may run at the
+ * same time need separate workspaces. vda_sequence_poll reads the status of
+ * their bounded waits.
+ */
+typedef struct vda_attention_config {
+  int N;           /* sequences, >= 1 */
+  int Hq;          /* query heads */
+  int Hkv;         /* key and value heads; divides Hq, Hq / Hkv <= 128 */
+  int d;           /* channels per head: 64 or 128 */
+  int Tq;          /* rows of Q, O (all sequences, and what lies behind them) */
+  int Tk;          /* rows of K, V */
+  long long q_row, k_row, v_row, o_row; /* elements between token rows */
+  float scale;     /* of the logits; > 0 */
+} vda_attention_config;
+
+/* Bytes of workspace vda_causal_attention needs for cfg (0: workspace may be NULL). Host-only. */
+vda_status vda_causal_attention_workspace(const vda_attention_config* cfg, size_t* bytes);
+
+/*
+ * Causal softmax attention with grouped heads. Sequence i has nq queries and nk
+ * keys; its last query stands at its last key, so query r sees keys
+ * 0 .. nk - nq + r:
+ *   o_r = sum_j p_rj v_j,  p_rj = exp(scale q_r.k_j) / sum_j' exp(scale q_r.k_j'),
+ * query head h with key head h / (Hq / Hkv). A query that sees no key gives 0
+ * (and lse = -infinity). With nq = 1 it is the step of generation: one new token
+ * of each sequence against its cache.
+ *   Q, O   [Tq, Hq, d] bf16       K, V  [Tk, Hkv, d] bf16
+ *   cu_q, cu_k  int32 [N + 1]: the sequences' rows of Q (O) and of K (V)
+ *   k_len  int32 [N] or NULL: where given, only the first k_len[i] rows of
+ *          sequence i's room cu_k[i] .. cu_k[i+1]-1 are its keys
+ *   lse    float32 [Tq, Hq] or NULL: log of the row's sum of exponentials
+ *   workspace 256-byte aligned, vda_causal_attention_workspace bytes
+ */
+vda_status vda_causal_attention(const vda_attention_config* cfg, const void* Q, const void* K, const void* V,
+                                const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* O, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace vda_causal_attention_backward needs for cfg. Host-only. */
+vda_status vda_causal_attention_backward_workspace(const vda_attention_config* cfg, size_t* bytes);
+
+/*
+ * Gradients of vda_causal_attention: given dO = dL/dO, the O and lse that the
+ * call returned for the same inputs, writes dL/dQ, dL/dK and dL/dV (the latter
+ * two summed over the query heads of a group). Results do not depend on the
+ * order of execution (no atomics). Keys that no query sees get 0.
+ *   O, dO     [Tq, Hq, d] bf16, rows o_row apart
+ *   dQ        [Tq, Hq, d], dK, dV [Tk, Hkv, d] bf16, contiguous; rows outside the
+ *             sequences (and behind k_len) are left as they were
+ *   workspace 256-byte aligned
+ */
+vda_status vda_causal_attention_backward(const vda_attention_config* cfg, const void* Q, const void* K,
+                                         const void* V, const void* O, const void* dO, const float* lse,
+                                         const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* dQ,
+                                         void* dK, void* dV, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct vda_decay_config {
+  int N;           /* sequences, 1 .. 65535 (vda_decay_attention_step: >= 1) */
+  int H;           /* heads */
+  int d;           /* channels of keys and of values: 64 or 128 */
+  int T;           /* rows of the token tensors (vda_decay_attention_step: N) */
+  long long q_row, k_row, v_row, o_row; /* elements between token rows (o_row: of O, and of dO) */
+  float scale;     /* of the output */
+} vda_decay_config;
+
+/* Bytes of workspace vda_decay_attention needs for cfg (0: workspace may be NULL). Host-only. */
+vda_status vda_decay_attention_workspace(const vda_decay_config* cfg, size_t* bytes);
+
+/*
+ * Linear attention whose state decays by a factor of each head: with
+ * a = exp(log_decay[h]) and S_0 the given state (zero when S0 is NULL),
+ *   S_t = a S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ * for the tokens of every sequence in order (the frame scan's orientation: S is
+ * d_v x d_k). S receives the state after the last token; for an empty sequence
+ * that is the state it had.
+ *   Q, K, V, O  [T, H, d] bf16        cu  int32 [N + 1]
+ *   log_decay   float32 [H], <= 0 (minus infinity: nothing is kept)
+ *   S0, S       float32 [N, H, d, d], contiguous; each may be NULL; S may be S0
+ */
+vda_status vda_decay_attention(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const int32_t* cu, const float* S0, void* O, float* S,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for one token of every sequence, the step of generation: row n of Q,
+ * K, V, O belongs to sequence n, whose state S[n] is updated in place. */
+vda_status vda_decay_attention_step(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                                    const float* log_decay, float* S, void* O, void* stream);
+
+/* Bytes of workspace vda_decay_attention_backward needs for cfg. Host-only. */
+vda_status vda_decay_attention_backward_workspace(const vda_decay_config* cfg, size_t* bytes);
+
+/*
+ * Gradients of vda_decay_attention: given dO = dL/dO and dS = dL/dS (NULL: zero),
+ * writes dL/dQ, dL/dK, dL/dV and dL/dS0 (NULL: not wanted). The decays are the
+ * heads' fixed factors: they get no gradient.
+ *   dO          [T, H, d] bf16, rows o_row apart
+ *   dQ, dK, dV  [T, H, d] bf16, contiguous; rows outside the sequences are left
+ *   dS, dS0     float32 [N, H, d, d]; dS0 may not be dS or S0
+ */
+vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
+                                        const void* dO, const float* log_decay, const int32_t* cu, const float* S0,
+                                        const float* dS, void* dQ, void* dK, void* dV, float* dS0, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Status of the prompt path's calls on the current device: synchronise `stream`,
+ * and return VDA_ERR_TIMEOUT if a bounded device-side wait of any of them gave up
+ * since the last poll (the word is cleared), VDA_OK otherwise. The word is kept
+ * by the library, one per device; the first of these calls on a device looks its
+ * address up, so make that one before any stream capture.
+ */
+vda_status vda_sequence_poll(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
