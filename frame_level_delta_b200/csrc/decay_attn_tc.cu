@@ -28,16 +28,23 @@
 // chunk and is added to X in registers: the tensor cores' accumulation rounds
 // toward zero, and over a long sequence that would pull the state down.
 //
-// What bounds it: the tensor work of a chunk is 3072 cycles (QK, PV, QX, and
-// three W parts, each 512 at d = 128), its four tiles take about 5700 cycles of
-// the HBM rate's share of one SM, so the copies decide when enough CTAs run.
-// Where (sequences x heads) leave SMs idle, long sequences are cut into
-// segments: a first launch forms every segment's own state from K and V alone,
-// a small kernel joins them in order, and the main launch starts each segment
-// from its state.
-//
-// Warps: 0 TMA, 1 MMA, 2-5 P and output rows, 6-13 V' and the state (a row of X
-// per thread pair: warps 6-9 the first half of its columns, 10-13 the second).
+// What bounds it: a chunk's four tiles (128 KB at d = 128) take about 5700 cycles
+// of one SM's share of the HBM rate; its products 3072 cycles of tensor work (QK,
+// PV, QX and three parts of W, 512 each); and shared memory, which carries their
+// operands, V' (read once, written three times) and the output tile, about as
+// long. None may wait for another, so each has its own warps, joined by barriers:
+//   warp 0 TMA loads; warp 1 issues QK, QX, PV; warp 2 issues W; warp 3 TMA stores;
+//   warps 4-11 make P and the output rows (half the columns each four warps);
+//   warps 12-19 make V' and hold the state (two threads to a row of X, half its
+//   columns each).
+// V' is made in steps of 2048 / D tokens, the two halves of warps 12-19 taking
+// turns with a buffer each, and the state of chunk c is taken up after their first
+// steps of chunk c + 1, so that its products have time to finish. Tiles go through a ring of five (d = 128); an output tile
+// is staged in the slot of the V tile it no longer needs and leaves by TMA.
+// Where (sequences x heads) leave SMs idle, long sequences are cut into segments:
+// a first launch forms every segment's own state from K and V alone, a small
+// kernel joins them in order, and the main launch starts each segment from its
+// state.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,10 +58,8 @@ namespace vda {
 
 namespace {
 
-constexpr int kC = 128;        // tokens per chunk
-constexpr int kThreads = 448;
-constexpr int kStateThreads = 256;
-constexpr int kQuarter = 32;   // tokens of V' per step
+constexpr int kC = 128;  // tokens per chunk
+constexpr int kThreads = 640;
 constexpr int kMaxJobs = 3;
 
 template <int D>
@@ -62,11 +67,18 @@ struct DaCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kC * D * 2;
   static constexpr int kRing = D == 128 ? 5 : 10;
-  static constexpr int kPartBytes = kQuarter * D * 2;  // one of the three parts of V'
+  static constexpr int kStep = 2048 / D;               // tokens of V' per step
+  static constexpr int kSteps = kC / kStep;            // steps per chunk
+  static constexpr int kPartBytes = kStep * D * 2;     // one of the three parts of V' (4 KB)
+  static constexpr int kVpBytes = 3 * kPartBytes;      // one buffer
   static constexpr int kVpOff = kRing * kTileBytes;
-  static constexpr int kXOff = kVpOff + 3 * kPartBytes;
-  static constexpr int kBarOff = kXOff + (D * D * 2 < 8192 ? 8192 : D * D * 2);
-  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static constexpr int kXOff = kVpOff + 2 * kVpBytes;
+  // X, or two more buffers of V' where no output is made. At d = 64 the upper 64
+  // rows of W are not part of the state; their operand is whatever follows a part:
+  // the next part, the next buffer, X, or room left for it.
+  static constexpr int kXBytes = D == 128 ? D * D * 2 : 2 * kVpBytes + kPartBytes;
+  static constexpr int kBarOff = kXOff + kXBytes;
+  static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
   static constexpr uint32_t kS1 = 0, kO1 = 128, kO2 = 256, kW = 384;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
@@ -74,10 +86,12 @@ struct DaCfg {
   static constexpr uint32_t kIdescQX = sm100::idesc_bf16_f32(128, D, false, false);
   static constexpr uint32_t kIdescW = sm100::idesc_bf16_f32(128, D, true, true);
   static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may use");
+  static_assert(D * D * 2 <= kXBytes && 2 * kVpBytes + (D == 64 ? kPartBytes : 0) <= kXBytes, "X's place is too small");
 };
 
 struct DaMaps {
-  CUtensorMap m[4];
+  CUtensorMap m[4];            // token tensors
+  CUtensorMap out[kMaxJobs];   // the jobs' outputs
 };
 
 struct DaJob {
@@ -119,11 +133,45 @@ __device__ __forceinline__ void chunk_tokens(int len, int reverse, int p0, int p
   hi = min(len, reverse ? (nch - p0) * kC : p1 * kC);
 }
 
+// x = hi + mid + lo, each a bf16 (the upper half of a word), exactly: 8 bits of
+// the 24 each, cut off, not rounded. Returns the packed pairs of two values.
+__device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const float2 neg = make_float2(-1.f, -1.f);
+  hi = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+  x = __ffma2_rn(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), neg, x);
+  mid = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+  x = __ffma2_rn(make_float2(__uint_as_float(mid << 16), __uint_as_float(mid & 0xffff0000u)), neg, x);
+  lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
+// Shared memory read where it stands: the weights do not change from chunk to
+// chunk, and hoisted out of the loop they would not fit the registers.
+__device__ __forceinline__ float shared_float(const float* p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(sm100::smem_u32(p)));
+  return v;
+}
+__device__ __forceinline__ float2 shared_float2(const float* p) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(sm100::smem_u32(p)));
+  return v;
+}
+// A value the compiler may not carry over from an earlier pass of a loop: the
+// issuing warps have few registers, and operands built from loop constants would
+// be kept in spilled ones.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
 template <int D, bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid_constant__ DaMaps maps,
                                                                     const __grid_constant__ DaArgs a) {
   using C = DaCfg<D>;
   using namespace sm100;
+  // Groups of four warps that make V', each with a buffer and every kMakers-th
+  // step. Where no output is made all four groups do, two buffers in X's place.
+  constexpr int kMakers = kStateOnly ? 4 : 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* sVp = smem + C::kVpOff;
@@ -134,17 +182,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   uint64_t* pfull = sfull + 1;
   uint64_t* odone = pfull + 1;
   uint64_t* oempty = odone + 1;
-  uint64_t* vpfull = oempty + 1;
-  uint64_t* vpempty = vpfull + 1;
-  uint64_t* wfull = vpempty + 1;
+  uint64_t* vpfull = oempty + 1;        // [kMakers]
+  uint64_t* vpempty = vpfull + kMakers; // [kMakers]
+  uint64_t* wfull = vpempty + kMakers;
   uint64_t* wempty = wfull + 1;
   uint64_t* xfull = wempty + 1;
   uint64_t* xempty = xfull + 1;
-  uint64_t* drain = xempty + 1;
+  uint64_t* ofull = xempty + 1;    // an output tile is staged
+  uint64_t* drain = ofull + 1;     // both issuing warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* v_read = tmem_slot + 2;  // chunks whose V tile V' has been made from
   int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
-  static_assert((2 * C::kRing + 11) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
+  float* pw = reinterpret_cast<float*>(scratch + 40);  // [64], see below
+  static_assert((2 * C::kRing + 10 + 2 * kMakers) * 8 + 16 + 160 + 256 + 16 <= 1024, "barrier block overflows its allowance");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int jb = blockIdx.x % a.njobs;
@@ -179,31 +230,45 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     tok = lo + cc * kC;
     n = min(kC, len - cc * kC);
   };
-  constexpr int kTiles = kStateOnly ? 2 : 3;  // ring tiles per chunk: (Q,) K, V
+  // Ring tiles per chunk: (Q,) K, V. A slot is free after two arrivals: of Q, two
+  // commits behind QX; of K, QK's and W's; of V, W's (V' has been read) and the
+  // output tile's.
+  constexpr int kTiles = kStateOnly ? 2 : 3;
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 1);
+      mbar_init(&rempty[i], 2);
     }
     mbar_init(sfull, 1);
-    mbar_init(pfull, 4);
+    mbar_init(pfull, 8);
     mbar_init(odone, 1);
-    mbar_init(oempty, 4);
-    mbar_init(vpfull, 8);
-    mbar_init(vpempty, 1);
+    mbar_init(oempty, 8);
+    for (int i = 0; i < kMakers; ++i) {
+      mbar_init(&vpfull[i], 4);
+      mbar_init(&vpempty[i], 1);
+    }
     mbar_init(wfull, 1);
     mbar_init(wempty, 8);
     mbar_init(xfull, 8);
     mbar_init(xempty, 1);
-    mbar_init(drain, 1);
+    mbar_init(ofull, 8);
+    mbar_init(drain, 2);
     *abort_flag = 0;
+    *v_read = 0;
     fence_mbar_init();
     if (!kStateOnly) prefetch_tmap(&maps.m[job.q]);
     prefetch_tmap(&maps.m[job.k]);
     prefetch_tmap(&maps.m[job.v]);
   }
-  if (warp == 1) {
+  // The weight of a pair is a power of the row's distance from the near edge of a
+  // block of 32 columns times one of the column's distance from that edge; on the
+  // diagonal, where the two would overflow apart, one power of less than 32.
+  if (warp == 2) {
+    pw[lane] = power(g2, rev ? lane : 31 - lane);
+    pw[32 + lane] = power(g2, lane);
+  }
+  if (warp == 3) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -216,136 +281,238 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     return mbar_wait(bar, n & 1, abort_flag, a.status, a.wait_ns);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool { return __all_sync(0xffffffffu, wait1(bar, n)); };
+  // Ring slot and use of tile u (counted from the end: 1 = V, 2 = K, 3 = Q) of chunk c.
+  auto slot_of = [&](int c, int u) { return ((c + 1) * kTiles - u) % C::kRing; };
+  auto use_of = [&](int c, int u) { return ((c + 1) * kTiles - u) / C::kRing; };
 
-  if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int c = 0; c < nch && ok; ++c) {
-        int tok, n;
-        chunk(c, tok, n);
-        for (int u = 0; u < kTiles && ok; ++u) {
-          const int which = kStateOnly ? u + 1 : u;
-          const CUtensorMap* m = &maps.m[which == 0 ? job.q : which == 1 ? job.k : job.v];
-          const int slot = issued % C::kRing;
-          if (!(ok = wait1(&rempty[slot], issued / C::kRing + 1))) break;
-          mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+  // One step of V' by a group of four warps: its 2048 / D tokens, 16 channels of a
+  // token to each thread. Steps start at a multiple of 8 tokens, so the swizzle of
+  // a token is the same in V's tile and in the buffer. `maker` is the group's number.
+  const int st = threadIdx.x % 128;
+  const int tl = st / (D / 16), ch0 = st % (D / 16) * 2;
+  const uint32_t sw0 = ((ch0 % 8) ^ (tl & 7)) * 16, sw1 = ((ch0 % 8 + 1) ^ (tl & 7)) * 16;
+  auto make_step = [&](int maker, int g) -> bool {
+    const int c = g / C::kSteps, q = g % C::kSteps;
+    int tok, n;
+    chunk(c, tok, n);
+    if (q < kMakers) {
+      if (!warp_wait(&rfull[slot_of(c, 1)], use_of(c, 1))) return false;
+      if (n < kC) {
+        // Key rows behind the sequence are zeroed (by every group: each signals steps of its own).
+        if (!warp_wait(&rfull[slot_of(c, 2)], use_of(c, 2))) return false;
+        if (st >= n) seq::zero_row(smem + slot_of(c, 2) * C::kTileBytes, C::kAtoms, st, kC);
+      }
+    }
+    const int j = q * C::kStep + tl;
+    const uint8_t* src = smem + slot_of(c, 1) * C::kTileBytes + (ch0 / 8) * (kC * 128) + j * 128;
+    uint4 raw[2] = {*reinterpret_cast<const uint4*>(src + sw0), *reinterpret_cast<const uint4*>(src + sw1)};
+    if (j >= n) raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+    const float w = j < n ? job.s_up * power(g2, rev ? j + 1 : n - 1 - j) : 0.f;
+    uint32_t out[2][3][4];  // made while the products of the group's last step still read its buffer
 #pragma unroll
-          for (int at = 0; at < C::kAtoms; ++at)
-            tma_load_3d(smem + slot * C::kTileBytes + at * (kC * 128), m, &rfull[slot], at * 64, h, tok);
-          ++issued;
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        split3(__fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)),
+                          make_float2(w, w)),
+               out[u][0][e], out[u][1][e], out[u][2][e]);
+    }
+    if (g >= kMakers && !warp_wait(&vpempty[maker], g / kMakers - 1)) return false;
+    uint8_t* dst = sVp + maker * C::kVpBytes + (ch0 / 8) * (C::kStep * 128) + tl * 128;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int p3 = 0; p3 < 3; ++p3)
+        *reinterpret_cast<uint4*>(dst + p3 * C::kPartBytes + (u ? sw1 : sw0)) =
+            make_uint4(out[u][p3][0], out[u][p3][1], out[u][p3][2], out[u][p3][3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&vpfull[maker]);
+    return true;
+  };
+
+  // 640 threads start with 96 registers each; the loading and issuing warps give
+  // half of theirs to the state's (48 + 2 x 96 + 2 x 120 = 480 = 5 x 96).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 0) {
+      if (seq::elect_one()) {
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+          int tok, n;
+          chunk(c, tok, n);
+          for (int u = kTiles; u >= 1; --u) {
+            const CUtensorMap* m = &maps.m[u == 3 ? job.q : u == 2 ? job.k : job.v];
+            const int slot = issued % C::kRing;
+            if (!(ok = wait1(&rempty[slot], issued / C::kRing + 1))) break;
+            mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+#pragma unroll
+            for (int at = 0; at < C::kAtoms; ++at)
+              tma_load_3d(smem + slot * C::kTileBytes + at * (kC * 128), m, &rfull[slot], at * 64, h, tok);
+            ++issued;
+          }
+        }
+      }
+    } else if (warp == 1) {
+      if (seq::elect_one()) {
+        bool ok = true;
+        if (!kStateOnly) {
+          for (int c = 0; c < nch; ++c) {
+            // The address field of a descriptor counts 16 bytes: steps are added to it.
+            const uint64_t dq = smem_desc_sw128(smem_u32(smem + slot_of(c, 3) * C::kTileBytes), 16, 1024);
+            const uint64_t dk = smem_desc_sw128(smem_u32(smem + slot_of(c, 2) * C::kTileBytes), 16, 1024);
+            const uint64_t dv = smem_desc_sw128(smem_u32(smem + slot_of(c, 1) * C::kTileBytes), kC * 128, 1024);
+            const uint64_t dx = smem_desc_sw128(opaque(smem_u32(sX)), 16, 1024);
+            const uint32_t tm = opaque(tmem);
+            if (!(ok = wait1(&rfull[slot_of(c, 3)], use_of(c, 3)) && wait1(&rfull[slot_of(c, 2)], use_of(c, 2)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
+              mma_f16(tm + C::kS1, dq + (off >> 4), dk + (off >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(sfull);
+            mma_commit(&rempty[slot_of(c, 2)]);
+            if (!(ok = wait1(xfull, c))) break;
+            if (c > 0 && !(ok = wait1(oempty, c - 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
+              const uint32_t xoff = (kk / 4) * (D * 128) + (kk % 4) * 32;
+              mma_f16(tm + C::kO2, dq + (off >> 4), dx + (xoff >> 4), C::kIdescQX, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(xempty);
+            mma_commit(&rempty[slot_of(c, 3)]);
+            mma_commit(&rempty[slot_of(c, 3)]);
+            if (!(ok = wait1(pfull, c) && wait1(&rfull[slot_of(c, 1)], use_of(c, 1)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kC / 16; ++kk)
+              mma_f16_ts(tm + C::kO1, tm + C::kS1 + (kk / 4) * 64 + (kk % 4) * 8, dv + kk * 128, C::kIdescPV, kk > 0 ? 1u : 0u);
+            mma_commit(odone);
+          }
+        }
+        mma_commit(drain);
+      }
+    } else if (warp == 2) {
+      if (seq::elect_one()) {
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+          const uint64_t dk = smem_desc_sw128(smem_u32(smem + slot_of(c, 2) * C::kTileBytes), kC * 128, 1024);
+          if (!(ok = wait1(&rfull[slot_of(c, 2)], use_of(c, 2)))) break;
+          for (int q = 0; q < C::kSteps; ++q) {
+            const int g = c * C::kSteps + q;
+            if (q == 0 && c > 0 && !(ok = wait1(wempty, c - 1))) break;
+            if (!(ok = wait1(&vpfull[g % kMakers], g / kMakers))) break;
+            tc_fence_after();
+            const uint64_t da = smem_desc_sw128(smem_u32(sVp + (g % kMakers) * C::kVpBytes), C::kStep * 128, 1024);
+#pragma unroll
+            for (int p3 = 0; p3 < 3; ++p3)
+#pragma unroll
+              for (int kk = 0; kk < C::kStep / 16; ++kk)
+                mma_f16(tmem + C::kW, da + (p3 * C::kPartBytes + kk * 2048) / 16,
+                        dk + (q * (C::kStep / 16) + kk) * 128, C::kIdescW, (q > 0 || p3 > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&vpempty[g % kMakers]);
+          }
+          if (!ok) break;
+          smem_release_u32(v_read, c + 1);
+          mma_commit(wfull);
+          mma_commit(&rempty[slot_of(c, 2)]);
+          mma_commit(&rempty[slot_of(c, 1)]);
+          if (kStateOnly) {
+            mma_commit(&rempty[slot_of(c, 2)]);
+            mma_commit(&rempty[slot_of(c, 1)]);
+          }
+        }
+        mma_commit(drain);
+      }
+    } else if (!kStateOnly) {
+      if (seq::elect_one()) {
+        // Whole tiles leave by TMA; of a ragged one the threads have stored the rows.
+        for (int c = 0; c < nch; ++c) {
+          int tok, n;
+          chunk(c, tok, n);
+          if (!wait1(ofull, c)) break;
+          if (n == kC) {
+#pragma unroll
+            for (int at = 0; at < C::kAtoms; ++at)
+              seq::tma_store_3d(&maps.out[jb], smem + slot_of(c, 1) * C::kTileBytes + at * (kC * 128), at * 64, h, tok);
+            seq::bulk_commit();
+            seq::bulk_wait_read0();
+          }
+          mbar_arrive(&rempty[slot_of(c, 1)]);
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int c = 0; c < nch && ok; ++c) {
-        const int base = c * kTiles;
-        const int pq = base, pk = base + kTiles - 2, pv = base + kTiles - 1;
-        const int slot_q = pq % C::kRing, slot_k = pk % C::kRing, slot_v = pv % C::kRing;
-        const uint32_t qb = smem_u32(smem + slot_q * C::kTileBytes);
-        const uint32_t kb = smem_u32(smem + slot_k * C::kTileBytes);
-        const uint32_t vb = smem_u32(smem + slot_v * C::kTileBytes);
-        // W += V'^T K over the 32 tokens of quarter q.
-        auto issue_w = [&](int q) -> bool {
-          if (!wait1(vpfull, 4 * c + q)) return false;
-          if (q == 0 && c > 0 && !wait1(wempty, c - 1)) return false;
-          tc_fence_after();
-          const uint32_t ab = smem_u32(sVp);
-#pragma unroll
-          for (int part3 = 0; part3 < 3; ++part3)
-#pragma unroll
-            for (int kk = 0; kk < kQuarter / 16; ++kk)
-              mma_f16(tmem + C::kW, smem_desc_sw128(ab + part3 * C::kPartBytes + kk * 2048, kQuarter * 128, 1024),
-                      smem_desc_sw128(kb + (q * 2 + kk) * 2048, kC * 128, 1024), C::kIdescW,
-                      (q > 0 || part3 > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(vpempty);
-          return true;
-        };
-        if (!(ok = wait1(&rfull[slot_k], pk / C::kRing))) break;
-        if (!kStateOnly) {
-          if (!(ok = wait1(&rfull[slot_q], pq / C::kRing))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
-            mma_f16(tmem + C::kS1, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024),
-                    C::kIdescS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(sfull);
-        }
-        if (!(ok = issue_w(0))) break;
-        if (!kStateOnly) {
-          if (!(ok = wait1(xfull, c))) break;
-          if (c > 0 && !(ok = wait1(oempty, c - 1))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
-            const uint32_t xoff = (kk / 4) * (D * 128) + (kk % 4) * 32;
-            mma_f16(tmem + C::kO2, smem_desc_sw128(qb + off, 16, 1024),
-                    smem_desc_sw128(smem_u32(sX) + xoff, 16, 1024), C::kIdescQX, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(xempty);
-          mma_commit(&rempty[slot_q]);
-        }
-        for (int q = 1; q < 4 && ok; ++q) ok = issue_w(q);
-        if (!ok) break;
-        mma_commit(wfull);
-        if (!kStateOnly) {
-          if (!(ok = wait1(pfull, c))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            mma_f16_ts(tmem + C::kO1, tmem + C::kS1 + kk * 8, smem_desc_sw128(vb + kk * 2048, kC * 128, 1024),
-                       C::kIdescPV, kk > 0 ? 1u : 0u);
-          mma_commit(odone);
-        }
-        mma_commit(&rempty[slot_k]);
-        mma_commit(&rempty[slot_v]);
-      }
-      mma_commit(drain);
-    }
-  } else if (warp < 6) {
-    // ---------------- P and the output rows: row i of the chunk per thread
+  } else if (warp < 12) {
+    // ---------------- P and the output rows: row i of the chunk per thread, half
+    // the columns. The packed P of a half lies in the first columns of its own
+    // logits, so no half overwrites what the other has yet to read.
     if (!kStateOnly) {
+      const int half = (warp - 4) / 4;
       const int quad = warp % 4;
       const int i = quad * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      const uint32_t sa = tmem + lane_off + C::kS1 + half * 64;
       bool ok = true;
       for (int c = 0; c < nch && ok; ++c) {
         int tok, n;
         chunk(c, tok, n);
         if (!(ok = warp_wait(sfull, c))) break;
         tc_fence_after();
-        // Weight a^|i - j| of the pairs this row sees: j <= i forward, i <= j < n backward.
-        const int j_lo = rev ? i : 0, j_hi = rev ? n : min(i + 1, n);
-        const float sg = rev ? g2 : -g2;
-        const float e0 = rev ? -g2 * (float)i : g2 * (float)i;
+        // Weight a^|i - j| of the pairs a row sees: j <= i forward, i <= j < n
+        // backward. Of the four 32-column blocks this warp's own is the diagonal;
+        // those before it (behind it) are seen whole, the others not at all.
+        uint32_t v[2][32];
+        seq::tmem_ld32(sa, v[0]);
+        seq::tmem_ld32(sa + 32, v[1]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t v[32], w[16];
-          seq::tmem_ld32(tmem + lane_off + C::kS1 + c4 * 32, v);
-          tmem_ld_wait();
+        for (int b2 = 0; b2 < 2; ++b2) {
+          const int c4 = half * 2 + b2, j0 = c4 * 32;
+          uint32_t w[16];
+          if (rev ? c4 < quad : c4 > quad) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float p[2];
+            for (int k = 0; k < 16; ++k) w[k] = 0u;
+          } else if (c4 == quad) {
+            const int edge = rev ? n - j0 : 32;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = c4 * 32 + 2 * k + e;
-              const float x = __uint_as_float(v[2 * k + e]) * seq::ex2_approx(fmaf(sg, (float)j, e0));
-              p[e] = (j >= j_lo && j < j_hi) ? x : 0.f;
+            for (int k = 0; k < 16; ++k) {
+              float p[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int j = 2 * k + e, far = rev ? j - lane : lane - j;
+                const float x = __uint_as_float(v[b2][j]) * shared_float(pw + 32 + (far & 31));
+                p[e] = (far >= 0 && j < edge) ? x : 0.f;
+              }
+              w[k] = seq::pack_bf16(p[0], p[1]);
             }
-            w[k] = seq::pack_bf16(p[0], p[1]);
+          } else {
+            const float base = rev ? power(g2, j0 - i) : power(g2, i - j0 - 31);
+            const float2 b = make_float2(base, base);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 x = __fmul2_rn(
+                  __fmul2_rn(make_float2(__uint_as_float(v[b2][2 * k]), __uint_as_float(v[b2][2 * k + 1])), b),
+                  shared_float2(pw + 2 * k));
+              w[k] = seq::pack_bf16(x.x, x.y);
+            }
+            if (rev && n < kC) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[k] = j0 + 2 * k >= n ? 0u : j0 + 2 * k + 1 >= n ? w[k] & 0xffffu : w[k];
+            }
           }
-          tmem_st16(tmem + lane_off + C::kS1 + c4 * 16, w);
+          tmem_st16(sa + b2 * 16, w);
         }
         tmem_st_wait();
+        uint8_t* vt = smem + slot_of(c, 1) * C::kTileBytes;
         if (n < kC) {
           // Value rows behind the sequence are zeroed: 0 x NaN is NaN.
-          const int pv = c * kTiles + kTiles - 1;
-          if (!(ok = warp_wait(&rfull[pv % C::kRing], pv / C::kRing))) break;
-          if (i >= n) seq::zero_row(smem + (pv % C::kRing) * C::kTileBytes, C::kAtoms, i, kC);
+          if (!(ok = warp_wait(&rfull[slot_of(c, 1)], use_of(c, 1)))) break;
+          if (i >= n) seq::zero_row(vt, C::kAtoms, i, kC);
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -355,37 +522,58 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         const float f = job.s_state * power(g2, rev ? n - 1 - i : i + 1);
         if (!(ok = warp_wait(odone, c))) break;
         tc_fence_after();
+        // A whole tile is staged where V was: P V is done with it, and V' when the
+        // W warp has counted the chunk (that chain may be a chunk ahead of this
+        // one, so it is a count and not a barrier's phase).
+        if (n == kC && !(ok = __all_sync(0xffffffffu, smem_wait_geq(v_read, c + 1, abort_flag, a.status, a.wait_ns))))
+          break;
         uint4* dst = reinterpret_cast<uint4*>(job.out + (long long)(tok + min(i, n - 1)) * job.out_row + h * D);
+        const float2 f2 = make_float2(f, f), s2 = make_float2(job.s_in, job.s_in);
 #pragma unroll
-        for (int c4 = 0; c4 < D / 32; ++c4) {
-          uint32_t v[32], x[32];
-          seq::tmem_ld32(tmem + lane_off + C::kO1 + c4 * 32, v);
-          seq::tmem_ld32(tmem + lane_off + C::kO2 + c4 * 32, x);
+        for (int u = 0; u < D / 64; ++u) {
+          const int col = half * (D / 2) + u * 32;
+          uint32_t y[32], x[32];
+          seq::tmem_ld32(tmem + lane_off + C::kO1 + col, y);
+          seq::tmem_ld32(tmem + lane_off + C::kO2 + col, x);
           tmem_ld_wait();
-          if (i < n) {
 #pragma unroll
-            for (int q8 = 0; q8 < 4; ++q8) {
-              uint32_t op[4];
+          for (int q8 = 0; q8 < 4; ++q8) {
+            uint32_t op[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = q8 * 8 + 2 * k;
-                op[k] = seq::pack_bf16(fmaf(f, __uint_as_float(x[e]), job.s_in * __uint_as_float(v[e])),
-                                       fmaf(f, __uint_as_float(x[e + 1]), job.s_in * __uint_as_float(v[e + 1])));
-              }
-              dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
+            for (int k = 0; k < 4; ++k) {
+              const int e = q8 * 8 + 2 * k;
+              const float2 o = __ffma2_rn(
+                  f2, make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                  __fmul2_rn(s2, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))));
+              op[k] = seq::pack_bf16(o.x, o.y);
+            }
+            const uint4 o4 = make_uint4(op[0], op[1], op[2], op[3]);
+            const int ch = col / 8 + q8;
+            if (n == kC) {
+              *reinterpret_cast<uint4*>(vt + (ch / 8) * (kC * 128) + i * 128 + (((ch % 8) ^ (i & 7)) * 16)) = o4;
+            } else if (i < n) {
+              dst[ch] = o4;
             }
           }
         }
         tc_fence_before();
+        if (n == kC) fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(oempty);
+        if (lane == 0) {
+          mbar_arrive(oempty);
+          mbar_arrive(ofull);
+        }
       }
+    } else {
+      const int maker = (warp - 4) / 4;
+      for (int g = maker; g < nch * C::kSteps; g += kMakers)
+        if (!make_step(maker, g)) break;
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---------------- V' and the state
     constexpr int kCols = D / 2;
-    const int st = threadIdx.x - (kThreads - kStateThreads);
-    const int half = (warp - 6) / 4;
+    const int half = (warp - 12) / 4;
     const int quad = warp % 4;
     const int row = quad * 32 + lane;  // row of X
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -429,80 +617,48 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(xfull);
     };
-    bool ok = true;
-    if (!kStateOnly && nch > 0) write_x();
-    for (int c = 0; c < nch && ok; ++c) {
+    // X' = a^n X + W of chunk c.
+    auto take_w = [&](int c) -> bool {
       int tok, n;
       chunk(c, tok, n);
-      const int pk = c * kTiles + kTiles - 2, pv = pk + 1;
-      uint8_t* vt = smem + (pv % C::kRing) * C::kTileBytes;
-      if (!(ok = warp_wait(&rfull[pv % C::kRing], pv / C::kRing))) break;
-      if (n < kC) {
-        if (!(ok = warp_wait(&rfull[pk % C::kRing], pk / C::kRing))) break;
-        if (st < kC && st >= n) seq::zero_row(smem + (pk % C::kRing) * C::kTileBytes, C::kAtoms, st, kC);
-      }
-      for (int q = 0; q < 4 && ok; ++q) {
-        const int vp = 4 * c + q;
-        // Eight threads to a token, D / 8 channels each.
-        const int tl = st / 8, j = q * kQuarter + tl;
-        constexpr int kCh = D / 64;  // 16-byte chunks per thread
-        uint4 raw[kCh];
-#pragma unroll
-        for (int u = 0; u < kCh; ++u) {
-          const int ch = (st % 8) * kCh + u;  // chunk of 8 channels
-          raw[u] = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kC * 128) + j * 128 + (((ch % 8) ^ (j & 7)) * 16));
-        }
-        const float w = j < n ? job.s_up * power(g2, rev ? j + 1 : n - 1 - j) : 0.f;
-        if (vp > 0 && !(ok = warp_wait(vpempty, vp - 1))) break;
-#pragma unroll
-        for (int u = 0; u < kCh; ++u) {
-          const int ch = (st % 8) * kCh + u;
-          const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-          uint32_t out[3][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(bits_bf162(in[e]));
-            float x = j < n ? f.x * w : 0.f, y = j < n ? f.y * w : 0.f;
-#pragma unroll
-            for (int p3 = 0; p3 < 3; ++p3) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-              out[p3][e] = bf162_bits(b);
-              const float2 r = __bfloat1622float2(b);
-              x -= r.x;
-              y -= r.y;
-            }
-          }
-#pragma unroll
-          for (int p3 = 0; p3 < 3; ++p3)
-            *reinterpret_cast<uint4*>(sVp + p3 * C::kPartBytes + (ch / 8) * (kQuarter * 128) + tl * 128 +
-                                      (((ch % 8) ^ (tl & 7)) * 16)) =
-                make_uint4(out[p3][0], out[p3][1], out[p3][2], out[p3][3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vpfull);
-      }
-      if (!ok) break;
-      // X' = a^n X + W
-      if (!(ok = warp_wait(wfull, c))) break;
+      if (!warp_wait(wfull, c)) return false;
       tc_fence_after();
       const float f = power(g2, n);
 #pragma unroll
-      for (int k4 = 0; k4 < kCols / 32; ++k4) {
-        uint32_t v[32];
-        seq::tmem_ld32(tmem + lane_off + C::kW + half * kCols + k4 * 32, v);
+      for (int k4 = 0; k4 < kCols / 16; ++k4) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lane_off + C::kW + half * kCols + k4 * 16, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) X[k4 * 32 + k] = fmaf(f, X[k4 * 32 + k], __uint_as_float(v[k]));
+        for (int k = 0; k < 16; k += 2) {
+          float* x = &X[k4 * 16 + k];
+          const float2 y = __ffma2_rn(make_float2(f, f), make_float2(x[0], x[1]),
+                                      make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+          x[0] = y.x;
+          x[1] = y.y;
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(wempty);
-      if (!kStateOnly && c + 1 < nch) {
-        if (!(ok = warp_wait(xempty, c))) break;  // Q X^T of this chunk has read the old X
+      return true;
+    };
+    bool ok = true;
+    if (!kStateOnly && nch > 0) write_x();
+    const int maker = kMakers - 2 + half;
+    for (int g = maker; g < nch * C::kSteps && ok; g += kMakers) {
+      const int c = g / C::kSteps;
+      // The first step of a chunk: the state of the last one first, so that W is
+      // free, then the step, then X for the chunk's QX (once the last has read it).
+      const bool first = g % C::kSteps < kMakers && c > 0;
+      if (first && !(ok = take_w(c - 1))) break;
+      if (!(ok = make_step(maker, g))) break;
+      if (first && !kStateOnly) {
+        if (!(ok = warp_wait(xempty, c - 1))) break;
         write_x();
       }
     }
+    if (ok && nch > 0) ok = take_w(nch - 1);
     float* last = kStateOnly ? seg_state : (part == nparts - 1 && job.last) ? job.last + st_off : nullptr;
     if (ok && last && has_row) {
 #pragma unroll
@@ -518,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     for (int i = max(0, issued - C::kRing); i < issued; ++i)
       mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
   }
-  if (warp == 1) {
+  if (warp == 3) {
     if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
     __syncwarp();
     tc_fence_after();
@@ -530,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
 // sequences that have several: block (sequence, head, job) x slices of the matrix.
 template <int D>
 __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DaArgs a) {
+  constexpr int kBatch = 8;
   __shared__ int first_s;
   const int sq = blockIdx.y;
   const int jb = blockIdx.x % a.njobs, h = (blockIdx.x / a.njobs) % a.H;
@@ -563,15 +720,24 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
       x = *reinterpret_cast<const float4*>(init + e);
   }
   const int nch = (len + kC - 1) / kC;
-  for (int p = 0; p < nparts; ++p) {
-    float4* w = reinterpret_cast<float4*>(
-        a.seg_state + (((long long)(first_s + p) * a.H + h) * a.njobs + jb) * (D * D) + e);
-    int t0, t1;
-    chunk_tokens(len, job.reverse, p * a.seg, min(nch, (p + 1) * a.seg), t0, t1);
-    const float4 y = p + 1 < nparts ? *w : make_float4(0.f, 0.f, 0.f, 0.f);
-    *w = x;
-    const float f = power(g2, t1 - t0);
-    x = make_float4(fmaf(f, x.x, y.x), fmaf(f, x.y, y.y), fmaf(f, x.z, y.z), fmaf(f, x.w, y.w));
+  const long long stride = (long long)a.H * a.njobs * (D * D);
+  float* base = a.seg_state + (((long long)first_s * a.H + h) * a.njobs + jb) * (D * D) + e;
+  for (int p0 = 0; p0 < nparts; p0 += kBatch) {  // the loads of a batch are in flight together
+    float4 y[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (p0 + u + 1 < nparts) y[u] = *reinterpret_cast<const float4*>(base + (p0 + u) * stride);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int p = p0 + u;
+      if (p >= nparts) break;
+      *reinterpret_cast<float4*>(base + p * stride) = x;
+      if (p + 1 == nparts) break;
+      int t0, t1;
+      chunk_tokens(len, job.reverse, p * a.seg, min(nch, (p + 1) * a.seg), t0, t1);
+      const float f = power(g2, t1 - t0);
+      x = make_float4(fmaf(f, x.x, y[u].x), fmaf(f, x.y, y[u].y), fmaf(f, x.z, y[u].z), fmaf(f, x.w, y[u].w));
+    }
   }
 }
 
@@ -646,15 +812,16 @@ __global__ void __launch_bounds__(256) decay_step_kernel(const vda_decay_config 
   }
 }
 
-constexpr int kMinSegChunks = 8;
+constexpr int kMinSegChunks = 4;
 
-// Chunks per segment. A sequence longer than half of one SM's share of the whole
-// work is cut, but not into less than kMinSegChunks (a segment reads its keys
-// and values twice, and starts from a state).
+// Chunks per segment: one SM's share of the whole work, so that a long sequence
+// is cut into about as many CTAs as there are SMs, but not into less than
+// kMinSegChunks (a segment reads its keys and values twice, and the launch that
+// forms the segments' states costs its start).
 int segment_chunks(const vda_decay_config& c, int njobs) {
   const long long chunks = ((long long)c.T + kC - 1) / kC + c.N / 2;
-  const long long share = chunks * c.H * njobs / 148;
-  return (int)std::min<long long>(1 << 20, std::max<long long>(kMinSegChunks, (share + 1) / 2));
+  const long long share = (chunks * c.H * njobs + 147) / 148;
+  return (int)std::min<long long>(1 << 20, std::max<long long>(kMinSegChunks, share));
 }
 long long segment_items(const vda_decay_config& c, int seg) { return (long long)c.T / ((long long)seg * kC) + c.N; }
 
@@ -676,6 +843,10 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
   for (int i = 0; i < nmaps; ++i) {
     uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)row[i] * 2};
     if ((e = make_tmap_bf16(&maps.m[i], ptr[i], 3, dims, str, box)) != cudaSuccess) return e;
+  }
+  for (int j = 0; j < a.njobs; ++j) {
+    uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)a.job[j].out_row * 2};
+    if ((e = make_tmap_bf16(&maps.out[j], a.job[j].out, 3, dims, str, box)) != cudaSuccess) return e;
   }
   const void* main_fn = reinterpret_cast<const void*>(decay_attn_tc_kernel<D, false>);
   const void* state_fn = reinterpret_cast<const void*>(decay_attn_tc_kernel<D, true>);

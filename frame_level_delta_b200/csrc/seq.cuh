@@ -58,6 +58,17 @@ __device__ __forceinline__ int find_item(int x, int N, int* scratch, Count count
   return scratch[33];
 }
 
+// One lane of a converged warp, chosen by the hardware.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -80,10 +91,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-// Zeroes 16-byte chunk c (of 8) of token row `row` in each of `atoms` boxes of
-// 128 token rows x 64 channels (128-byte rows; a whole row is zeroed, so the
-// swizzle does not matter). For rows past a sequence's end: they hold another
-// sequence's values or whatever lies behind the last one, and 0 x NaN is NaN.
+// 3-D tiled bulk tensor copy shared -> global (the issuing thread's bulk group),
+// and the wait until the group's copies have read shared memory.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(sm100::smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Zeroes token row `row` in each of `atoms` boxes of 64 channels (128-byte rows;
+// whole rows, so the swizzle does not matter). For rows past a sequence's end:
+// they hold another sequence's values or whatever lies behind the last one, and
+// 0 x NaN is NaN.
 __device__ __forceinline__ void zero_row(uint8_t* tile, int atoms, int row, int rows_per_atom) {
   for (int at = 0; at < atoms; ++at) {
     uint4* p = reinterpret_cast<uint4*>(tile + (size_t)at * rows_per_atom * 128 + row * 128);
