@@ -19,28 +19,31 @@
 // in one launch and share their tensors' reads through L2.
 //
 // One CTA takes one (sequence, head, job, segment) and walks the segment's
-// chunks with X in registers. Per chunk: S1 = Q K^T and, masked and weighted,
-// P = bf16 in TMEM; O1 = P V; O2 = Q X^T with X rounded to bf16 in shared memory
-// (operand type of the tensor cores; outputs are bf16, so each of the two
-// roundings adds what the output's own rounding is); W = V'^T K, where
-// V' = a^(n-1-j) v_j enters as three bf16 parts (24 bits together), so that the
-// state, which is fp32 outside, keeps fp32 accuracy. W starts from zero in every
-// chunk and is added to X in registers: the tensor cores' accumulation rounds
-// toward zero, and over a long sequence that would pull the state down.
+// chunks with X in registers. Per chunk: S1 = Q K^T; masked and weighted, P = bf16
+// in TMEM; O = Q X^T with X rounded to bf16 in shared memory, scaled by a^(i+1) in
+// TMEM, then O += P V (outputs are bf16, so each of the two operand roundings adds
+// what the output's own rounding is); W = V'^T K, where V' = a^(n-1-j) v_j enters
+// as three bf16 parts (24 bits together), so that the state, which is fp32
+// outside, keeps fp32 accuracy. W starts from zero in every chunk and is added to
+// X in registers: the tensor cores' accumulation rounds toward zero, and over a
+// long sequence that would pull the state down.
 //
-// What bounds it: a chunk's four tiles (128 KB at d = 128) take about 5700 cycles
-// of one SM's share of the HBM rate; its products 3072 cycles of tensor work (QK,
-// PV, QX and three parts of W, 512 each); and shared memory, which carries their
-// operands, V' (read once, written three times) and the output tile, about as
-// long. None may wait for another, so each has its own warps, joined by barriers:
+// V'^T is the left operand from TMEM: transposed loads of V's tile give a thread
+// pairs of tokens of a channel, the words of that operand. (As a shared
+// memory operand it cost 96 KB of stores a chunk and twice the tensor time: the
+// products then read both operands at the rate of shared memory.)
+//
+// What bounds it: a chunk's four tiles (128 KB at d = 128) take about 2.9 us of
+// one SM's share of the HBM rate; its products about 4500 cycles (QK and QX with
+// both operands in shared memory 1100 each, PV 560, three parts of W 1700). No
+// part may wait for another, so each has its own warps, joined by barriers:
 //   warp 0 TMA loads; warp 1 issues QK, QX, PV; warp 2 issues W; warp 3 TMA stores;
 //   warps 4-11 make P and the output rows (half the columns each four warps);
 //   warps 12-19 make V' and hold the state (two threads to a row of X, half its
 //   columns each).
-// V' is made in steps of 2048 / D tokens, the two halves of warps 12-19 taking
-// turns with a buffer each, and the state of chunk c is taken up after their first
-// steps of chunk c + 1, so that its products have time to finish. Tiles go through a ring of five (d = 128); an output tile
-// is staged in the slot of the V tile it no longer needs and leaves by TMA.
+// V' is made in steps of 32 tokens, the two halves of warps 12-19 taking turns
+// with a buffer each. Two chunks' tiles are in shared memory; an output tile is
+// staged in the slot of the V tile it no longer needs and leaves by TMA.
 // Where (sequences x heads) leave SMs idle, long sequences are cut into segments:
 // a first launch forms every segment's own state from K and V alone, a small
 // kernel joins them in order, and the main launch starts each segment from its
@@ -66,27 +69,18 @@ template <int D>
 struct DaCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kC * D * 2;
-  static constexpr int kRing = D == 128 ? 5 : 10;
-  static constexpr int kStep = 2048 / D;               // tokens of V' per step
-  static constexpr int kSteps = kC / kStep;            // steps per chunk
-  static constexpr int kPartBytes = kStep * D * 2;     // one of the three parts of V' (4 KB)
-  static constexpr int kVpBytes = 3 * kPartBytes;      // one buffer
-  static constexpr int kVpOff = kRing * kTileBytes;
-  static constexpr int kXOff = kVpOff + 2 * kVpBytes;
-  // X, or two more buffers of V' where no output is made. At d = 64 the upper 64
-  // rows of W are not part of the state; their operand is whatever follows a part:
-  // the next part, the next buffer, X, or room left for it.
-  static constexpr int kXBytes = D == 128 ? D * D * 2 : 2 * kVpBytes + kPartBytes;
-  static constexpr int kBarOff = kXOff + kXBytes;
-  static constexpr int kSmemBytes = kBarOff + 1024 + 1024;
-  static constexpr uint32_t kS1 = 0, kO1 = 128, kO2 = 256, kW = 384;
+  static constexpr int kStep = 32;           // tokens of V' per step
+  static constexpr int kSteps = kC / kStep;  // steps per chunk
+  static constexpr int kXOff = 6 * kTileBytes;
+  static constexpr int kBarOff = kXOff + D * D * 2;
+  static constexpr int kSmemBytes = kBarOff + 2048 + 1024;
+  // TMEM columns: S1, O, W; V' in 64 columns a buffer (three parts of 16).
+  static constexpr uint32_t kS1 = 0, kO = 128, kW = 256, kVp = 384;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescPV = sm100::idesc_bf16_f32(128, D, false, true);
   static constexpr uint32_t kIdescQX = sm100::idesc_bf16_f32(128, D, false, false);
-  static constexpr uint32_t kIdescW = sm100::idesc_bf16_f32(128, D, true, true);
   static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may use");
-  static_assert(D * D * 2 <= kXBytes && 2 * kVpBytes + (D == 64 ? kPartBytes : 0) <= kXBytes, "X's place is too small");
 };
 
 struct DaMaps {
@@ -170,32 +164,34 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   using C = DaCfg<D>;
   using namespace sm100;
   // Groups of four warps that make V', each with a buffer and every kMakers-th
-  // step. Where no output is made all four groups do, two buffers in X's place.
+  // step. Where no output is made all four groups do, in the columns S1 and O leave.
   constexpr int kMakers = kStateOnly ? 4 : 2;
+  constexpr uint32_t kVpCol = kStateOnly ? 0 : C::kVp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
-  uint8_t* sVp = smem + C::kVpOff;
   uint8_t* sX = smem + C::kXOff;
-  uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* rempty = rfull + C::kRing;
-  uint64_t* sfull = rempty + C::kRing;
+  uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [2][3] chunk parity; Q, K, V
+  uint64_t* rempty = rfull + 6;
+  uint64_t* sfull = rempty + 6;
   uint64_t* pfull = sfull + 1;
-  uint64_t* odone = pfull + 1;
+  uint64_t* qxdone = pfull + 1;
+  uint64_t* oscaled = qxdone + 1;
+  uint64_t* odone = oscaled + 1;
   uint64_t* oempty = odone + 1;
-  uint64_t* vpfull = oempty + 1;        // [kMakers]
-  uint64_t* vpempty = vpfull + kMakers; // [kMakers]
+  uint64_t* vpfull = oempty + 1;  // [kMakers]
+  uint64_t* vpempty = vpfull + kMakers;
   uint64_t* wfull = vpempty + kMakers;
   uint64_t* wempty = wfull + 1;
   uint64_t* xfull = wempty + 1;
-  uint64_t* xempty = xfull + 1;
-  uint64_t* ofull = xempty + 1;    // an output tile is staged
-  uint64_t* drain = ofull + 1;     // both issuing warps
+  uint64_t* ofull = xfull + 1;  // an output tile is staged
+  uint64_t* drain = ofull + 1;  // both issuing warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* v_read = tmem_slot + 2;  // chunks whose V tile V' has been made from
   int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
-  float* pw = reinterpret_cast<float*>(scratch + 40);  // [64], see below
-  static_assert((2 * C::kRing + 10 + 2 * kMakers) * 8 + 16 + 160 + 256 + 16 <= 1024, "barrier block overflows its allowance");
+  float* pw = reinterpret_cast<float*>(scratch + 40);  // [32 + 64], see below
+  float* wt = pw + 96;                                 // [256] weights of V' in a whole chunk, then zeros
+  static_assert((23 + 2 * kMakers) * 8 + 16 + 160 + 4 * (96 + 256) + 16 <= 2048, "barrier block overflows its allowance");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int jb = blockIdx.x % a.njobs;
@@ -230,18 +226,20 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     tok = lo + cc * kC;
     n = min(kC, len - cc * kC);
   };
-  // Ring tiles per chunk: (Q,) K, V. A slot is free after two arrivals: of Q, two
-  // commits behind QX; of K, QK's and W's; of V, W's (V' has been read) and the
-  // output tile's.
-  constexpr int kTiles = kStateOnly ? 2 : 3;
+  // A slot is free after two arrivals: of Q, two commits behind QX; of K, QK's and
+  // W's; of V, W's (V' has been read) and the output tile's.
+  auto slot_of = [&](int c, int t) { return (c & 1) * 3 + t; };
+  auto tile_of = [&](int c, int t) { return smem + slot_of(c, t) * C::kTileBytes; };
 
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < C::kRing; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(&rfull[i], 1);
       mbar_init(&rempty[i], 2);
     }
     mbar_init(sfull, 1);
     mbar_init(pfull, 8);
+    mbar_init(qxdone, 1);
+    mbar_init(oscaled, 8);
     mbar_init(odone, 1);
     mbar_init(oempty, 8);
     for (int i = 0; i < kMakers; ++i) {
@@ -251,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     mbar_init(wfull, 1);
     mbar_init(wempty, 8);
     mbar_init(xfull, 8);
-    mbar_init(xempty, 1);
     mbar_init(ofull, 8);
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -263,10 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   }
   // The weight of a pair is a power of the row's distance from the near edge of a
   // block of 32 columns times one of the column's distance from that edge; on the
-  // diagonal, where the two would overflow apart, one power of less than 32.
+  // diagonal, where the two would overflow apart, one power of their distance, 0
+  // where the row does not see the column: entry 32 + column - row of the second
+  // table. The factor of P V goes with it.
   if (warp == 2) {
-    pw[lane] = power(g2, rev ? lane : 31 - lane);
-    pw[32 + lane] = power(g2, lane);
+    pw[lane] = job.s_in * power(g2, rev ? lane : 31 - lane);
+    pw[32 + lane] = rev || lane == 0 ? 0.f : job.s_in * power(g2, 32 - lane);
+    pw[64 + lane] = rev || lane == 0 ? job.s_in * power(g2, lane) : 0.f;
+  }
+  if (warp >= 4 && warp < 12) {
+    const int j = threadIdx.x - 128;
+    wt[j] = j >= kC ? 0.f : job.s_up * power(g2, rev ? j + 1 : kC - 1 - j);
   }
   if (warp == 3) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -276,57 +280,73 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int issued = 0;
+  int loaded = 0;  // chunks whose copies have been issued
   auto wait1 = [&](uint64_t* bar, uint32_t n) -> bool {  // n-th phase of the barrier, n = 0, 1, ...
-    return mbar_wait(bar, n & 1, abort_flag, a.status, a.wait_ns);
+    return seq::bar_wait(bar, n & 1, abort_flag, a.status, (uint32_t)a.wait_ns);
   };
-  auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool { return __all_sync(0xffffffffu, wait1(bar, n)); };
-  // Ring slot and use of tile u (counted from the end: 1 = V, 2 = K, 3 = Q) of chunk c.
-  auto slot_of = [&](int c, int u) { return ((c + 1) * kTiles - u) % C::kRing; };
-  auto use_of = [&](int c, int u) { return ((c + 1) * kTiles - u) / C::kRing; };
+  auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool {
+    return seq::warp_wait(bar, n & 1, abort_flag, a.status, (uint32_t)a.wait_ns);
+  };
 
-  // One step of V' by a group of four warps: its 2048 / D tokens, 16 channels of a
-  // token to each thread. Steps start at a multiple of 8 tokens, so the swizzle of
-  // a token is the same in V's tile and in the buffer. `maker` is the group's number.
-  const int st = threadIdx.x % 128;
-  const int tl = st / (D / 16), ch0 = st % (D / 16) * 2;
-  const uint32_t sw0 = ((ch0 % 8) ^ (tl & 7)) * 16, sw1 = ((ch0 % 8 + 1) ^ (tl & 7)) * 16;
+  // One step of V' by a group of four warps: its 32 tokens, 32 value channels (TMEM
+  // lanes) to each warp. `maker` is the group's number.
+  const int quad = warp % 4;
+  const int row = quad * 32 + lane;
+  const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+  // Each thread's row of V's tile for the transposed loads: eight tokens by eight
+  // channels to a matrix, matrices (token group 0, 1) x (channel group 2 b, 2 b + 1).
+  // A thread then holds pairs of tokens of channel lane / 4: words of the operand,
+  // and the lanes and columns of a 16 x 128-bit store.
+  const uint32_t v_off = (row / 64) * (kC * 128) + ((lane / 16) * 8 + lane % 8) * 128;
+  const uint32_t v_chunk = (((quad & 1) * 4 + (lane / 8) % 2) ^ (lane % 8)) * 16;
   auto make_step = [&](int maker, int g) -> bool {
     const int c = g / C::kSteps, q = g % C::kSteps;
     int tok, n;
     chunk(c, tok, n);
-    if (q < kMakers) {
-      if (!warp_wait(&rfull[slot_of(c, 1)], use_of(c, 1))) return false;
-      if (n < kC) {
-        // Key rows behind the sequence are zeroed (by every group: each signals steps of its own).
-        if (!warp_wait(&rfull[slot_of(c, 2)], use_of(c, 2))) return false;
-        if (st >= n) seq::zero_row(smem + slot_of(c, 2) * C::kTileBytes, C::kAtoms, st, kC);
+    if (!warp_wait(&rfull[slot_of(c, 2)], c >> 1)) return false;
+    if (n < kC && q < kMakers) {
+      // Key and value rows behind the sequence are zeroed (by every group: each
+      // reads and signals steps of its own).
+      if (!warp_wait(&rfull[slot_of(c, 1)], c >> 1)) return false;
+      if (row >= n) {
+        seq::zero_row(tile_of(c, 1), C::kAtoms, row, kC);
+        seq::zero_row(tile_of(c, 2), C::kAtoms, row, kC);
       }
-    }
-    const int j = q * C::kStep + tl;
-    const uint8_t* src = smem + slot_of(c, 1) * C::kTileBytes + (ch0 / 8) * (kC * 128) + j * 128;
-    uint4 raw[2] = {*reinterpret_cast<const uint4*>(src + sw0), *reinterpret_cast<const uint4*>(src + sw1)};
-    if (j >= n) raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-    const float w = j < n ? job.s_up * power(g2, rev ? j + 1 : n - 1 - j) : 0.f;
-    uint32_t out[2][3][4];  // made while the products of the group's last step still read its buffer
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        split3(__fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)),
-                          make_float2(w, w)),
-               out[u][0][e], out[u][1][e], out[u][2][e]);
+      fence_proxy_async_smem();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + maker) : "memory");
     }
     if (g >= kMakers && !warp_wait(&vpempty[maker], g / kMakers - 1)) return false;
-    uint8_t* dst = sVp + maker * C::kVpBytes + (ch0 / 8) * (C::kStep * 128) + tl * 128;
+    tc_fence_after();
+    if (row < D) {
+      // Forward, a token's weight goes by its distance from the chunk's end: in a
+      // ragged chunk the table is read from further on.
+      const float* w = wt + (rev ? 0 : kC - n) + q * C::kStep + (lane % 4) * 2;
+      const uint8_t* src = tile_of(c, 2) + v_off + q * (C::kStep * 128);
+      uint32_t dst = tmem + lane_off + kVpCol + maker * 64;
+      uint32_t chunk_at = v_chunk;
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {  // channels 16 b .. 16 b + 15 of the warp's 32
+        uint32_t out[3][8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+        for (int t2 = 0; t2 < 2; ++t2) {  // tokens 16 t2 .. 16 t2 + 15
+          uint32_t in[4];
+          seq::ldmatrix4_trans(in, src + t2 * 2048 + chunk_at);
 #pragma unroll
-      for (int p3 = 0; p3 < 3; ++p3)
-        *reinterpret_cast<uint4*>(dst + p3 * C::kPartBytes + (u ? sw1 : sw0)) =
-            make_uint4(out[u][p3][0], out[u][p3][1], out[u][p3][2], out[u][p3][3]);
-    fence_proxy_async_smem();
+          for (int m = 0; m < 4; ++m) {  // tokens 8 (m / 2) .., channels 8 (m % 2) ..
+            const int o = t2 * 4 + m, j = t2 * 16 + (m / 2) * 8;
+            split3(__fmul2_rn(make_float2(__uint_as_float(in[m] << 16), __uint_as_float(in[m] & 0xffff0000u)),
+                              make_float2(w[j], w[j + 1])),
+                   out[0][o], out[1][o], out[2][o]);
+          }
+        }
+#pragma unroll
+        for (int p3 = 0; p3 < 3; ++p3) seq::tmem_st_16x128b_x4(dst + p3 * 16, out[p3]);
+        dst += 16u << 16;
+        chunk_at ^= 32;  // two 16-byte chunks on
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&vpfull[maker]);
     return true;
@@ -342,16 +362,22 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         for (int c = 0; c < nch && ok; ++c) {
           int tok, n;
           chunk(c, tok, n);
-          for (int u = kTiles; u >= 1; --u) {
-            const CUtensorMap* m = &maps.m[u == 3 ? job.q : u == 2 ? job.k : job.v];
-            const int slot = issued % C::kRing;
-            if (!(ok = wait1(&rempty[slot], issued / C::kRing + 1))) break;
-            mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+          for (int t = kStateOnly ? 1 : 0; t < 3; ++t) {
+            const CUtensorMap* m = &maps.m[t == 0 ? job.q : t == 1 ? job.k : job.v];
+            uint64_t* full = &rfull[slot_of(c, t)];
+            if (!(ok = wait1(&rempty[slot_of(c, t)], (c >> 1) + 1))) break;
+            mbar_arrive_expect_tx(full, C::kTileBytes);
 #pragma unroll
             for (int at = 0; at < C::kAtoms; ++at)
-              tma_load_3d(smem + slot * C::kTileBytes + at * (kC * 128), m, &rfull[slot], at * 64, h, tok);
-            ++issued;
+              tma_load_3d(tile_of(c, t) + at * (kC * 128), m, full, at * 64, h, tok);
+            loaded = c * 3 + t + 1;
           }
+        }
+        if (*abort_flag) {
+          // Let every issued copy land before the CTA's shared memory is released.
+          for (int i = max(0, loaded - 6); i < loaded; ++i)
+            if (!kStateOnly || i % 3 != 0)
+              mbar_wait(&rfull[slot_of(i / 3, i % 3)], (i / 6) & 1, nullptr, a.status, (uint32_t)a.wait_ns);
         }
       }
     } else if (warp == 1) {
@@ -360,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         if (!kStateOnly) {
           for (int c = 0; c < nch; ++c) {
             // The address field of a descriptor counts 16 bytes: steps are added to it.
-            const uint64_t dq = smem_desc_sw128(smem_u32(smem + slot_of(c, 3) * C::kTileBytes), 16, 1024);
-            const uint64_t dk = smem_desc_sw128(smem_u32(smem + slot_of(c, 2) * C::kTileBytes), 16, 1024);
-            const uint64_t dv = smem_desc_sw128(smem_u32(smem + slot_of(c, 1) * C::kTileBytes), kC * 128, 1024);
+            const uint64_t dq = smem_desc_sw128(smem_u32(tile_of(c, 0)), 16, 1024);
+            const uint64_t dk = smem_desc_sw128(smem_u32(tile_of(c, 1)), 16, 1024);
+            const uint64_t dv = smem_desc_sw128(smem_u32(tile_of(c, 2)), kC * 128, 1024);
             const uint64_t dx = smem_desc_sw128(opaque(smem_u32(sX)), 16, 1024);
             const uint32_t tm = opaque(tmem);
-            if (!(ok = wait1(&rfull[slot_of(c, 3)], use_of(c, 3)) && wait1(&rfull[slot_of(c, 2)], use_of(c, 2)))) break;
+            if (!(ok = wait1(&rfull[slot_of(c, 0)], c >> 1) && wait1(&rfull[slot_of(c, 1)], c >> 1))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -373,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
               mma_f16(tm + C::kS1, dq + (off >> 4), dk + (off >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
             }
             mma_commit(sfull);
-            mma_commit(&rempty[slot_of(c, 2)]);
+            mma_commit(&rempty[slot_of(c, 1)]);
             if (!(ok = wait1(xfull, c))) break;
             if (c > 0 && !(ok = wait1(oempty, c - 1))) break;
             tc_fence_after();
@@ -381,16 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
               const uint32_t xoff = (kk / 4) * (D * 128) + (kk % 4) * 32;
-              mma_f16(tm + C::kO2, dq + (off >> 4), dx + (xoff >> 4), C::kIdescQX, kk > 0 ? 1u : 0u);
+              mma_f16(tm + C::kO, dq + (off >> 4), dx + (xoff >> 4), C::kIdescQX, kk > 0 ? 1u : 0u);
             }
-            mma_commit(xempty);
-            mma_commit(&rempty[slot_of(c, 3)]);
-            mma_commit(&rempty[slot_of(c, 3)]);
-            if (!(ok = wait1(pfull, c) && wait1(&rfull[slot_of(c, 1)], use_of(c, 1)))) break;
+            mma_commit(qxdone);
+            mma_commit(&rempty[slot_of(c, 0)]);
+            mma_commit(&rempty[slot_of(c, 0)]);
+            if (!(ok = wait1(pfull, c) && wait1(oscaled, c) && wait1(&rfull[slot_of(c, 2)], c >> 1))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kC / 16; ++kk)
-              mma_f16_ts(tm + C::kO1, tm + C::kS1 + (kk / 4) * 64 + (kk % 4) * 8, dv + kk * 128, C::kIdescPV, kk > 0 ? 1u : 0u);
+              mma_f16_ts(tm + C::kO, tm + C::kS1 + (kk / 4) * 64 + (kk % 4) * 8, dv + kk * 128, C::kIdescPV, 1u);
             mma_commit(odone);
           }
         }
@@ -400,30 +426,31 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       if (seq::elect_one()) {
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
-          const uint64_t dk = smem_desc_sw128(smem_u32(smem + slot_of(c, 2) * C::kTileBytes), kC * 128, 1024);
-          if (!(ok = wait1(&rfull[slot_of(c, 2)], use_of(c, 2)))) break;
+          const uint64_t dk = smem_desc_sw128(smem_u32(tile_of(c, 1)), kC * 128, 1024);
+          if (!(ok = wait1(&rfull[slot_of(c, 1)], c >> 1))) break;
+#pragma unroll 1
           for (int q = 0; q < C::kSteps; ++q) {
-            const int g = c * C::kSteps + q;
+            const int g = c * C::kSteps + q, maker = g % kMakers;
+            if (!(ok = wait1(&vpfull[maker], g / kMakers))) break;
             if (q == 0 && c > 0 && !(ok = wait1(wempty, c - 1))) break;
-            if (!(ok = wait1(&vpfull[g % kMakers], g / kMakers))) break;
             tc_fence_after();
-            const uint64_t da = smem_desc_sw128(smem_u32(sVp + (g % kMakers) * C::kVpBytes), C::kStep * 128, 1024);
+            const uint32_t av = tmem + kVpCol + maker * 64;
 #pragma unroll
             for (int p3 = 0; p3 < 3; ++p3)
 #pragma unroll
               for (int kk = 0; kk < C::kStep / 16; ++kk)
-                mma_f16(tmem + C::kW, da + (p3 * C::kPartBytes + kk * 2048) / 16,
-                        dk + (q * (C::kStep / 16) + kk) * 128, C::kIdescW, (q > 0 || p3 > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&vpempty[g % kMakers]);
+                mma_f16_ts(tmem + C::kW, av + p3 * 16 + kk * 8, dk + (q * (C::kStep / 16) + kk) * 128, C::kIdescPV,
+                           (q > 0 || p3 > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&vpempty[maker]);
           }
           if (!ok) break;
           smem_release_u32(v_read, c + 1);
           mma_commit(wfull);
-          mma_commit(&rempty[slot_of(c, 2)]);
           mma_commit(&rempty[slot_of(c, 1)]);
+          mma_commit(&rempty[slot_of(c, 2)]);
           if (kStateOnly) {
-            mma_commit(&rempty[slot_of(c, 2)]);
             mma_commit(&rempty[slot_of(c, 1)]);
+            mma_commit(&rempty[slot_of(c, 2)]);
           }
         }
         mma_commit(drain);
@@ -438,24 +465,24 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
           if (n == kC) {
 #pragma unroll
             for (int at = 0; at < C::kAtoms; ++at)
-              seq::tma_store_3d(&maps.out[jb], smem + slot_of(c, 1) * C::kTileBytes + at * (kC * 128), at * 64, h, tok);
+              seq::tma_store_3d(&maps.out[jb], tile_of(c, 2) + at * (kC * 128), at * 64, h, tok);
             seq::bulk_commit();
             seq::bulk_wait_read0();
           }
-          mbar_arrive(&rempty[slot_of(c, 1)]);
+          mbar_arrive(&rempty[slot_of(c, 2)]);
         }
       }
     }
+    __syncwarp();
   } else if (warp < 12) {
     // ---------------- P and the output rows: row i of the chunk per thread, half
     // the columns. The packed P of a half lies in the first columns of its own
     // logits, so no half overwrites what the other has yet to read.
     if (!kStateOnly) {
       const int half = (warp - 4) / 4;
-      const int quad = warp % 4;
-      const int i = quad * 32 + lane;
-      const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+      const int i = row;
       const uint32_t sa = tmem + lane_off + C::kS1 + half * 64;
+      const uint32_t oa = tmem + lane_off + C::kO + half * (D / 2);
       bool ok = true;
       for (int c = 0; c < nch && ok; ++c) {
         int tok, n;
@@ -465,61 +492,76 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         // Weight a^|i - j| of the pairs a row sees: j <= i forward, i <= j < n
         // backward. Of the four 32-column blocks this warp's own is the diagonal;
         // those before it (behind it) are seen whole, the others not at all.
-        uint32_t v[2][32];
-        seq::tmem_ld32(sa, v[0]);
-        seq::tmem_ld32(sa + 32, v[1]);
-        tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
         for (int b2 = 0; b2 < 2; ++b2) {
           const int c4 = half * 2 + b2, j0 = c4 * 32;
           uint32_t w[16];
           if (rev ? c4 < quad : c4 > quad) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) w[k] = 0u;
-          } else if (c4 == quad) {
-            const int edge = rev ? n - j0 : 32;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float p[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int j = 2 * k + e, far = rev ? j - lane : lane - j;
-                const float x = __uint_as_float(v[b2][j]) * shared_float(pw + 32 + (far & 31));
-                p[e] = (far >= 0 && j < edge) ? x : 0.f;
-              }
-              w[k] = seq::pack_bf16(p[0], p[1]);
-            }
           } else {
-            const float base = rev ? power(g2, j0 - i) : power(g2, i - j0 - 31);
-            const float2 b = make_float2(base, base);
+            uint32_t v[32];
+            seq::tmem_ld32(sa + b2 * 32, v);
+            tmem_ld_wait();
+            if (c4 == quad) {
+              const float* t = pw + 64 - lane;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 x = __fmul2_rn(
-                  __fmul2_rn(make_float2(__uint_as_float(v[b2][2 * k]), __uint_as_float(v[b2][2 * k + 1])), b),
-                  shared_float2(pw + 2 * k));
-              w[k] = seq::pack_bf16(x.x, x.y);
+              for (int k = 0; k < 16; ++k) {
+                const float wx = shared_float(t + 2 * k), wy = shared_float(t + 2 * k + 1);
+                w[k] = seq::pack_bf16(wx != 0.f ? __uint_as_float(v[2 * k]) * wx : 0.f,
+                                      wy != 0.f ? __uint_as_float(v[2 * k + 1]) * wy : 0.f);
+              }
+            } else {
+              const float base = power(g2, rev ? j0 - i : i - j0 - 31);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 x = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
+                                                       make_float2(base, base)),
+                                            shared_float2(pw + 2 * k));
+                w[k] = seq::pack_bf16(x.x, x.y);
+              }
             }
-            if (rev && n < kC) {
+            if (n < j0 + 32) {  // columns behind the sequence
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                w[k] = j0 + 2 * k >= n ? 0u : j0 + 2 * k + 1 >= n ? w[k] & 0xffffu : w[k];
+              for (int k = 0; k < 16; ++k) w[k] = j0 + 2 * k >= n ? 0u : j0 + 2 * k + 1 >= n ? w[k] & 0xffffu : w[k];
             }
           }
           tmem_st16(sa + b2 * 16, w);
         }
         tmem_st_wait();
-        uint8_t* vt = smem + slot_of(c, 1) * C::kTileBytes;
+        uint8_t* vt = tile_of(c, 2);
         if (n < kC) {
           // Value rows behind the sequence are zeroed: 0 x NaN is NaN.
-          if (!(ok = warp_wait(&rfull[slot_of(c, 1)], use_of(c, 1)))) break;
+          if (!(ok = warp_wait(&rfull[slot_of(c, 2)], c >> 1))) break;
           if (i >= n) seq::zero_row(vt, C::kAtoms, i, kC);
           fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull);
-        // Output: o_i = s_in O1 + s_state a^(i+1) O2 (a^(distance from the end) backward).
+        // The state's part of the output: a^(i+1) forward, a^(distance from the
+        // end) backward.
         const float f = job.s_state * power(g2, rev ? n - 1 - i : i + 1);
+        if (!(ok = warp_wait(qxdone, c))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int u = 0; u < D / 64; ++u) {
+          uint32_t y[32];
+          seq::tmem_ld32(oa + u * 32, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 x =
+                __fmul2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), make_float2(f, f));
+            y[k] = __float_as_uint(x.x);
+            y[k + 1] = __float_as_uint(x.y);
+          }
+          seq::tmem_st32(oa + u * 32, y);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oscaled);
         if (!(ok = warp_wait(odone, c))) break;
         tc_fence_after();
         // A whole tile is staged where V was: P V is done with it, and V' when the
@@ -528,27 +570,19 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         if (n == kC && !(ok = __all_sync(0xffffffffu, smem_wait_geq(v_read, c + 1, abort_flag, a.status, a.wait_ns))))
           break;
         uint4* dst = reinterpret_cast<uint4*>(job.out + (long long)(tok + min(i, n - 1)) * job.out_row + h * D);
-        const float2 f2 = make_float2(f, f), s2 = make_float2(job.s_in, job.s_in);
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < D / 64; ++u) {
-          const int col = half * (D / 2) + u * 32;
-          uint32_t y[32], x[32];
-          seq::tmem_ld32(tmem + lane_off + C::kO1 + col, y);
-          seq::tmem_ld32(tmem + lane_off + C::kO2 + col, x);
+          uint32_t y[32];
+          seq::tmem_ld32(oa + u * 32, y);
           tmem_ld_wait();
 #pragma unroll
           for (int q8 = 0; q8 < 4; ++q8) {
             uint32_t op[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = q8 * 8 + 2 * k;
-              const float2 o = __ffma2_rn(
-                  f2, make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                  __fmul2_rn(s2, make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1]))));
-              op[k] = seq::pack_bf16(o.x, o.y);
-            }
+            for (int k = 0; k < 4; ++k)
+              op[k] = seq::pack_bf16(__uint_as_float(y[q8 * 8 + 2 * k]), __uint_as_float(y[q8 * 8 + 2 * k + 1]));
             const uint4 o4 = make_uint4(op[0], op[1], op[2], op[3]);
-            const int ch = col / 8 + q8;
+            const int ch = half * (D / 16) + u * 4 + q8;
             if (n == kC) {
               *reinterpret_cast<uint4*>(vt + (ch / 8) * (kC * 128) + i * 128 + (((ch % 8) ^ (i & 7)) * 16)) = o4;
             } else if (i < n) {
@@ -574,10 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     // ---------------- V' and the state
     constexpr int kCols = D / 2;
     const int half = (warp - 12) / 4;
-    const int quad = warp % 4;
-    const int row = quad * 32 + lane;  // row of X
-    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const bool has_row = row < D;
+    const bool has_row = row < D;  // row of X
     float X[kCols];
     {
       const bool joined = !kStateOnly && nparts > 1;
@@ -654,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       if (first && !(ok = take_w(c - 1))) break;
       if (!(ok = make_step(maker, g))) break;
       if (first && !kStateOnly) {
-        if (!(ok = warp_wait(xempty, c - 1))) break;
+        if (!(ok = warp_wait(qxdone, c - 1))) break;
         write_x();
       }
     }
@@ -670,12 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   // ---------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && threadIdx.x == 0) {
-    for (int i = max(0, issued - C::kRing); i < issued; ++i)
-      mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
-  }
   if (warp == 3) {
-    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
+    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, (uint32_t)a.wait_ns);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);

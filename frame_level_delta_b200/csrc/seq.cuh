@@ -69,6 +69,47 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// Bounded wait for the phase with the given parity, with mbar_wait's rules, in few
+// instructions: a kernel whose warps have different roles runs several loops at
+// once, and their code has to fit the instruction caches together (with
+// mbar_wait's longer loop and everything unrolled, the linear attention's working
+// warps spent 8 to 10 cycles an instruction). The try is given a time to sleep
+// (10 us); the clock's lower word serves limits below 4 s.
+__device__ __forceinline__ bool try_wait_asleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(10000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                         uint32_t limit_ns) {
+  const uint32_t t0 = globaltimer_lo();
+  while (!try_wait_asleep(bar, parity)) {
+    if (*abort) return false;
+    if (globaltimer_lo() - t0 > limit_ns) {
+      *abort = 1;
+      *reinterpret_cast<volatile uint32_t*>(status) = (uint32_t)VDA_ERR_TIMEOUT;
+      return false;
+    }
+  }
+  return true;
+}
+// The same by all lanes of a warp, which goes on only if all of them saw the phase.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                          uint32_t limit_ns) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort, status, limit_ns));
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -89,6 +130,34 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 16 lanes x 16 columns from the fragments of 8 x 8 matrices: word 2 i (2 i + 1) of
+// a thread goes to lane thread / 4 (+ 8), column 4 i + thread % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l gives the address of row
+// l % 8 of matrix l / 8 and receives values (2 (l % 4), 2 (l % 4) + 1) of column
+// l / 4 of each.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(sm100::smem_u32(p))
+               : "memory");
 }
 
 // 3-D tiled bulk tensor copy shared -> global (the issuing thread's bulk group),
