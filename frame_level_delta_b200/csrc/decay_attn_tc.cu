@@ -39,9 +39,9 @@
 // part may wait for another, so each has its own warps, joined by barriers:
 //   warp 0 TMA loads; warp 1 issues QK, QX, PV; warp 2 issues W; warp 3 TMA stores;
 //   warps 4-11 make P and the output rows (half the columns each four warps);
-//   warps 12-19 make V' and hold the state (two threads to a row of X, half its
-//   columns each).
-// V' is made in steps of 32 tokens, the two halves of warps 12-19 taking turns
+//   warps 12-19 hold the state (two threads to a row of X, half its columns each);
+//   warps 20-27 make V'.
+// V' is made in steps of 32 tokens, the two halves of warps 20-27 taking turns
 // with a buffer each. Two chunks' tiles are in shared memory; an output tile is
 // staged in the slot of the V tile it no longer needs and leaves by TMA.
 // Where (sequences x heads) leave SMs idle, long sequences are cut into segments:
@@ -62,7 +62,7 @@ namespace vda {
 namespace {
 
 constexpr int kC = 128;  // tokens per chunk
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr int kMaxJobs = 3;
 
 template <int D>
@@ -352,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     return true;
   };
 
-  // 640 threads start with 96 registers each; the loading and issuing warps give
-  // half of theirs to the state's (48 + 2 x 96 + 2 x 120 = 480 = 5 x 96).
+  // 896 threads start with 72 registers each; the loading, issuing and V' warps give
+  // some of theirs to the others (40 + 2 x 80 + 2 x 96 + 2 x 56 = 504 = 7 x 72).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       if (seq::elect_one()) {
         bool ok = true;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             const uint32_t tm = opaque(tmem);
             if (!(ok = wait1(&rfull[slot_of(c, 0)], c >> 1) && wait1(&rfull[slot_of(c, 1)], c >> 1))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
               mma_f16(tm + C::kS1, dq + (off >> 4), dk + (off >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             if (!(ok = wait1(xfull, c))) break;
             if (c > 0 && !(ok = wait1(oempty, c - 1))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk / 4) * (kC * 128) + (kk % 4) * 32;
               const uint32_t xoff = (kk / 4) * (D * 128) + (kk % 4) * 32;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             mma_commit(&rempty[slot_of(c, 0)]);
             if (!(ok = wait1(pfull, c) && wait1(oscaled, c) && wait1(&rfull[slot_of(c, 2)], c >> 1))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < kC / 16; ++kk)
               mma_f16_ts(tm + C::kO, tm + C::kS1 + (kk / 4) * 64 + (kk % 4) * 8, dv + kk * 128, C::kIdescPV, 1u);
             mma_commit(odone);
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             if (q == 0 && c > 0 && !(ok = wait1(wempty, c - 1))) break;
             tc_fence_after();
             const uint32_t av = tmem + kVpCol + maker * 64;
-#pragma unroll
+#pragma unroll 1
             for (int p3 = 0; p3 < 3; ++p3)
 #pragma unroll
               for (int kk = 0; kk < C::kStep / 16; ++kk)
@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     }
     __syncwarp();
   } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ---------------- P and the output rows: row i of the chunk per thread, half
     // the columns. The packed P of a half lies in the first columns of its own
     // logits, so no half overwrites what the other has yet to read.
@@ -564,48 +565,49 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         if (lane == 0) mbar_arrive(oscaled);
         if (!(ok = warp_wait(odone, c))) break;
         tc_fence_after();
+        // O into registers first: the next chunk's QX may then take its columns.
+        uint32_t op[D / 64][16];
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          uint32_t y[32];
+          seq::tmem_ld32(oa + u * 32, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            op[u][k] = seq::pack_bf16(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
         // A whole tile is staged where V was: P V is done with it, and V' when the
         // W warp has counted the chunk (that chain may be a chunk ahead of this
         // one, so it is a count and not a barrier's phase).
         if (n == kC && !(ok = __all_sync(0xffffffffu, smem_wait_geq(v_read, c + 1, abort_flag, a.status, a.wait_ns))))
           break;
         uint4* dst = reinterpret_cast<uint4*>(job.out + (long long)(tok + min(i, n - 1)) * job.out_row + h * D);
-#pragma unroll 1
-        for (int u = 0; u < D / 64; ++u) {
-          uint32_t y[32];
-          seq::tmem_ld32(oa + u * 32, y);
-          tmem_ld_wait();
 #pragma unroll
-          for (int q8 = 0; q8 < 4; ++q8) {
-            uint32_t op[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              op[k] = seq::pack_bf16(__uint_as_float(y[q8 * 8 + 2 * k]), __uint_as_float(y[q8 * 8 + 2 * k + 1]));
-            const uint4 o4 = make_uint4(op[0], op[1], op[2], op[3]);
-            const int ch = half * (D / 16) + u * 4 + q8;
-            if (n == kC) {
-              *reinterpret_cast<uint4*>(vt + (ch / 8) * (kC * 128) + i * 128 + (((ch % 8) ^ (i & 7)) * 16)) = o4;
-            } else if (i < n) {
-              dst[ch] = o4;
-            }
+        for (int q8 = 0; q8 < D / 16; ++q8) {
+          const uint32_t* o = &op[q8 / 4][q8 % 4 * 4];
+          const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
+          const int ch = half * (D / 16) + q8;
+          if (n == kC) {
+            *reinterpret_cast<uint4*>(vt + (ch / 8) * (kC * 128) + i * 128 + (((ch % 8) ^ (i & 7)) * 16)) = o4;
+          } else if (i < n) {
+            dst[ch] = o4;
           }
         }
-        tc_fence_before();
         if (n == kC) fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(oempty);
-          mbar_arrive(ofull);
-        }
+        if (lane == 0) mbar_arrive(ofull);
       }
     } else {
       const int maker = (warp - 4) / 4;
       for (int g = maker; g < nch * C::kSteps; g += kMakers)
         if (!make_step(maker, g)) break;
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-    // ---------------- V' and the state
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    // ---------------- the state
     constexpr int kCols = D / 2;
     const int half = (warp - 12) / 4;
     const bool has_row = row < D;  // row of X
@@ -676,26 +678,25 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     };
     bool ok = true;
     if (!kStateOnly && nch > 0) write_x();
-    const int maker = kMakers - 2 + half;
-    for (int g = maker; g < nch * C::kSteps && ok; g += kMakers) {
-      const int c = g / C::kSteps;
-      // The first step of a chunk: the state of the last one first, so that W is
-      // free, then the step, then X for the chunk's QX (once the last has read it).
-      const bool first = g % C::kSteps < kMakers && c > 0;
-      if (first && !(ok = take_w(c - 1))) break;
-      if (!(ok = make_step(maker, g))) break;
-      if (first && !kStateOnly) {
-        if (!(ok = warp_wait(qxdone, c - 1))) break;
+    for (int c = 0; c < nch && ok; ++c) {
+      if (!(ok = take_w(c))) break;
+      if (!kStateOnly && c + 1 < nch) {
+        if (!(ok = warp_wait(qxdone, c))) break;  // Q X^T of this chunk has read the old X
         write_x();
       }
     }
-    if (ok && nch > 0) ok = take_w(nch - 1);
     float* last = kStateOnly ? seg_state : (part == nparts - 1 && job.last) ? job.last + st_off : nullptr;
     if (ok && last && has_row) {
 #pragma unroll
       for (int k = 0; k < kCols; k += 4)
         *reinterpret_cast<float4*>(last + row * D + half * kCols + k) = make_float4(X[k], X[k + 1], X[k + 2], X[k + 3]);
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ---------------- V'
+    const int maker = kMakers - 2 + (warp - 20) / 4;
+    for (int g = maker; g < nch * C::kSteps; g += kMakers)
+      if (!make_step(maker, g)) break;
   }
 
   // ---------------- teardown
