@@ -64,7 +64,7 @@ struct CbArgs {
   const float2* stat;  // [Hkv][Tq][G] (lse log2(e), D)
   __nv_bfloat16 *dQ, *dK, *dV;
   uint32_t* status;
-  unsigned long long wait_ns;
+  uint32_t wait_ns;
 };
 
 __device__ __forceinline__ void key_range(const CbArgs& a, int i, int& lo, int& n) {
@@ -74,28 +74,46 @@ __device__ __forceinline__ void key_range(const CbArgs& a, int i, int& lo, int& 
   if (a.k_len) n = min(n, max(__ldg(a.k_len + i), 0));
 }
 
-// One warp per row (token, query head).
+// D / 8 threads per row (token, query head), 16 bytes each; kPerThread rows in
+// flight per thread.
 template <int D>
 __global__ void __launch_bounds__(256) attn_rowdot_kernel(const __nv_bfloat16* O, const __nv_bfloat16* dO,
                                                           long long o_row, const float* lse, float2* stat, int Tq,
                                                           int Hq, int G) {
-  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= (long long)Tq * Hq) return;
-  const long long tok = row / Hq;
-  const int h = (int)(row % Hq);
-  const long long at = tok * o_row + (long long)h * D + lane * (D / 32);
-  float s = 0.f;
+  constexpr int kLanes = D / 8, kRows = 256 / kLanes, kPerThread = 4;
+  const int part = threadIdx.x % kLanes;
+  const long long rows = (long long)Tq * Hq;
+  const long long row0 = (long long)blockIdx.x * (kRows * kPerThread) + threadIdx.x / kLanes;
+  uint4 x[kPerThread], y[kPerThread];
 #pragma unroll
-  for (int e = 0; e < D / 32; e += 2) {
-    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(O + at + e));
-    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(dO + at + e));
-    s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+  for (int u = 0; u < kPerThread; ++u) {
+    const long long row = row0 + u * kRows;
+    if (row < rows) {
+      const long long at = row / Hq * o_row + row % Hq * D + part * 8;
+      x[u] = __ldcs(reinterpret_cast<const uint4*>(O + at));
+      y[u] = __ldg(reinterpret_cast<const uint4*>(dO + at));
+    }
   }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lane == 0)
-    stat[((long long)(h / G) * Tq + tok) * G + h % G] = make_float2(lse[row] * 1.4426950408889634f, s);
+  for (int u = 0; u < kPerThread; ++u) {
+    const long long row = row0 + u * kRows;
+    float s = 0.f;
+    if (row < rows) {
+      const uint32_t a[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, b[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), s);
+        s = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(b[e] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (part == 0 && row < rows) {
+      const long long tok = row / Hq;
+      const int h = (int)(row % Hq);
+      stat[((long long)(h / G) * Tq + tok) * G + h % G] = make_float2(lse[row] * 1.4426950408889634f, s);
+    }
+  }
 }
 
 // Barriers and bookkeeping both kernels share.
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTileBytes;
   uint8_t* sR = smem + C::kRingOff;
-  float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
+  float* stat = reinterpret_cast<float*>(smem + C::kStatOff);  // per stage -lse log2(e), then -D
   CbBars<D> b(smem + C::kBarOff);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -208,16 +226,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   int issued = 0;
-  bool own_issued = false;
+  // After a wait gave up: let every issued copy land before the CTA's shared memory is released.
+  auto land = [&](int n) {
+    if (!*b.abort_flag) return;
+    mbar_wait(b.own, 0, nullptr, a.status, a.wait_ns);
+    for (int i = max(0, n - C::kRing); i < n; ++i)
+      mbar_wait(&b.rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
+  };
   auto wait1 = [&](uint64_t* bar, uint32_t n) -> bool {
-    return mbar_wait(bar, n & 1, b.abort_flag, a.status, a.wait_ns);
+    return seq::bar_wait(bar, n & 1, b.abort_flag, a.status, a.wait_ns);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool { return __all_sync(0xffffffffu, wait1(bar, n)); };
 
   if (warp == 0) {
     // ---------------- TMA producer, and the rows' (lse, D)
     if (n_it > 0) {
-      if (lane == 0) {
+      if (seq::elect_one()) {
         mbar_arrive_expect_tx(b.own, 2 * C::kTileBytes);
 #pragma unroll
         for (int at = 0; at < C::kAtoms; ++at) {
@@ -225,14 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sV + at * (kTile * 128), &mV, b.own, at * 64, hk, k_lo + k0);
         }
       }
-      own_issued = true;
       bool ok = true;
       for (int i = 0; i < n_it && ok; ++i) {
         const int t0 = (i0 + i) * a.tpt;
         for (int u = 0; u < 2 && ok; ++u) {
           const int slot = issued % C::kRing;
           if (!(ok = warp_wait(&b.rempty[slot], issued / C::kRing + 1))) break;
-          if (lane == 0) {
+          if (seq::elect_one()) {
             mbar_arrive_expect_tx(&b.rfull[slot], (uint32_t)rows * 128u * C::kAtoms);
 #pragma unroll
             for (int at = 0; at < C::kAtoms; ++at)
@@ -248,27 +271,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = u * 32 + lane;
-          stat[(i & 1) * kTile + r] = r < live ? src[r] : make_float2(0.f, 0.f);
+          const float2 v = r < live ? src[r] : make_float2(0.f, 0.f);
+          stat[(i & 1) * 2 * kTile + r] = -v.x;
+          stat[(i & 1) * 2 * kTile + kTile + r] = -v.y;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.stfull[i & 1]);
       }
+      land(issued);
     }
   } else if (warp == 1) {
-    if (lane == 0 && n_it > 0) {
-      bool ok = wait1(b.own, 0);
+    if (seq::elect_one()) {
+      bool ok = n_it > 0 && wait1(b.own, 0);
       auto slot_of = [&](int i, int u) { return (2 * i + u) % C::kRing; };
       // S^T (u = 0: K Q^T) or dP^T (u = 1: V dO^T) of tile i.
       auto issue_sd = [&](int i, int u) -> bool {
         const int slot = slot_of(i, u);
         if (!wait1(&b.rfull[slot], (2 * i + u) / C::kRing)) return false;
         tc_fence_after();
-        const uint32_t ab = smem_u32(u ? sV : sK), bb = smem_u32(sR + slot * C::kTileBytes);
+        // The address field of a descriptor counts 16 bytes: steps are added to it.
+        const uint64_t da = smem_desc_sw128(smem_u32(u ? sV : sK), 16, 1024);
+        const uint64_t db = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
-          mma_f16(tmem + (u ? kDP : kS), smem_desc_sw128(ab + off, 16, 1024), smem_desc_sw128(bb + off, 16, 1024),
-                  C::kIdescS, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) / 16;
+          mma_f16(tmem + (u ? kDP : kS), da + off, db + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
         mma_commit(u ? b.dpfull : &b.sfull[0]);
         return true;
@@ -277,11 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_g = [&](int i, int u) -> bool {
         if (!wait1(u ? b.dsfull : b.pfull, i)) return false;
         tc_fence_after();
-        const uint32_t bb = smem_u32(sR + slot_of(i, 1 - u) * C::kTileBytes);
+        const uint64_t db = smem_desc_sw128(smem_u32(sR + slot_of(i, 1 - u) * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + (u ? kDK : kDV), tmem + (u ? kDP : kS) + (kk / 4) * 64 + (kk % 4) * 8,
-                     smem_desc_sw128(bb + kk * 2048, kTile * 128, 1024), C::kIdescG, (i > 0 || kk > 0) ? 1u : 0u);
+          mma_f16_ts(tmem + (u ? kDK : kDV), tmem + (u ? kDP : kS) + (kk / 4) * 64 + (kk % 4) * 8, db + kk * 128,
+                     C::kIdescG, (i > 0 || kk > 0) ? 1u : 0u);
         return true;
       };
       ok = ok && issue_sd(0, 0) && issue_sd(0, 1);
@@ -294,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i + 1 < n_it && !(ok = issue_sd(i + 1, 1))) break;
       }
       if (ok) mma_commit(b.done);
+      mma_commit(b.drain);
     }
-    if (lane == 0) mma_commit(b.drain);
   } else {
     // ---------------- elementwise: key row per thread, 64 query columns
     const int half = (warp - 2) / 4;
@@ -313,24 +340,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = warp_wait(&b.stfull[i & 1], i / 2))) break;
       if (!(ok = warp_wait(&b.sfull[0], i))) break;
       tc_fence_after();
-      const float2* st = stat + (i & 1) * kTile + half * 64;
-      float p[64];
+      const float* st = stat + (i & 1) * 2 * kTile + half * 64;
+      float2 p[32];
       // First column that sees this row's key: token >= key - shift.
-      const int first = full ? 0 : max(0, (key - shift - t0)) * a.G - half * 64;
-      const int end = full ? 64 : min(a.tpt, nq - t0) * a.G - half * 64;
+      const int first = max(0, (key - shift - t0)) * a.G - half * 64;
+      const int end = min(a.tpt, nq - t0) * a.G - half * 64;
+      auto mask = [&](int c, uint32_t w) -> uint32_t {  // columns c, c + 1
+        return (c >= first && c < end ? w & 0xffffu : 0u) | (c + 1 >= first && c + 1 < end ? w & 0xffff0000u : 0u);
+      };
+      const float2 sl2 = make_float2(a.sl, a.sl);
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
         uint32_t v[32], w[16];
         seq::tmem_ld32(sa + c2 * 32, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int c = c2 * 32 + k;
-          const float e = seq::ex2_approx(fmaf(__uint_as_float(v[k]), a.sl, -st[c].x));
-          p[c] = (c >= first && c < end) ? e : 0.f;
+        for (int k = 0; k < 16; k += 2) {
+          const float4 l = *reinterpret_cast<const float4*>(st + c2 * 32 + 2 * k);
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2,
+                                      make_float2(l.x, l.y));
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])), sl2,
+                                      make_float2(l.z, l.w));
+          p[c2 * 16 + k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
+          p[c2 * 16 + k + 1] = make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = seq::pack_bf16(p[c2 * 32 + 2 * k], p[c2 * 32 + 2 * k + 1]);
+        for (int k = 0; k < 16; ++k) w[k] = seq::pack_bf16(p[c2 * 16 + k].x, p[c2 * 16 + k].y);
+        if (!full) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = mask(c2 * 32 + 2 * k, w[k]);
+        }
         tmem_st16(sa + c2 * 16, w);
       }
       tmem_st_wait();
@@ -352,15 +391,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         seq::tmem_ld32(da + c2 * 32, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int c = c2 * 32 + 2 * k;
-          float d0 = p[c] * (__uint_as_float(v[2 * k]) - st[c].y);
-          float d1 = p[c + 1] * (__uint_as_float(v[2 * k + 1]) - st[c + 1].y);
-          if (!full) {
-            d0 = (c >= first && c < end) ? d0 : 0.f;
-            d1 = (c + 1 >= first && c + 1 < end) ? d1 : 0.f;
-          }
-          w[k] = seq::pack_bf16(d0, d1);
+        for (int k = 0; k < 16; k += 2) {
+          const float4 l = *reinterpret_cast<const float4*>(st + kTile + c2 * 32 + 2 * k);
+          const float2 x = __fmul2_rn(p[c2 * 16 + k], __fadd2_rn(make_float2(__uint_as_float(v[2 * k]),
+                                                                             __uint_as_float(v[2 * k + 1])),
+                                                                 make_float2(l.x, l.y)));
+          const float2 y = __fmul2_rn(p[c2 * 16 + k + 1], __fadd2_rn(make_float2(__uint_as_float(v[2 * k + 2]),
+                                                                                 __uint_as_float(v[2 * k + 3])),
+                                                                     make_float2(l.z, l.w)));
+          w[k] = seq::pack_bf16(x.x, x.y);
+          w[k + 1] = seq::pack_bf16(y.x, y.y);
+        }
+        if (!full) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = mask(c2 * 32 + 2 * k, w[k]);
         }
         tmem_st16(da + c2 * 16, w);
       }
@@ -402,11 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (*b.abort_flag && threadIdx.x == 0) {
-    if (own_issued) mbar_wait(b.own, 0, nullptr, a.status, a.wait_ns);
-    for (int i = max(0, issued - C::kRing); i < issued; ++i)
-      mbar_wait(&b.rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
-  }
   if (warp == 1) {
     if (lane == 0) mbar_wait(b.drain, 0, nullptr, a.status, a.wait_ns);
     __syncwarp();
@@ -470,21 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   int issued = 0;
-  bool own_issued = false;
+  // After a wait gave up: let every issued copy land before the CTA's shared memory is released.
+  auto land = [&](int n) {
+    if (!*b.abort_flag) return;
+    mbar_wait(b.own, 0, nullptr, a.status, a.wait_ns);
+    for (int i = max(0, n - C::kRing); i < n; ++i)
+      mbar_wait(&b.rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
+  };
   auto wait1 = [&](uint64_t* bar, uint32_t n) -> bool {
-    return mbar_wait(bar, n & 1, b.abort_flag, a.status, a.wait_ns);
+    return seq::bar_wait(bar, n & 1, b.abort_flag, a.status, a.wait_ns);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool { return __all_sync(0xffffffffu, wait1(bar, n)); };
 
   if (warp == 0) {
-    if (lane == 0 && n_it > 0) {
+    if (n_it > 0 && seq::elect_one()) {
       mbar_arrive_expect_tx(b.own, 2u * rows * 128u * C::kAtoms);
 #pragma unroll
       for (int at = 0; at < C::kAtoms; ++at) {
         tma_load_3d(sQ + at * (kTile * 128), &mQ, b.own, at * 64, hk * a.G, q_lo + t0);
         tma_load_3d(sG + at * (kTile * 128), &mG, b.own, at * 64, hk * a.G, q_lo + t0);
       }
-      own_issued = true;
       bool ok = true;
       for (int i = 0; i < n_it && ok; ++i)
         for (int u = 0; u < 2 && ok; ++u) {
@@ -497,23 +541,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         k_lo + i * kTile);
           ++issued;
         }
+      land(issued);
     }
   } else if (warp == 1) {
-    if (lane == 0 && n_it > 0) {
-      bool ok = wait1(b.own, 0);
+    if (seq::elect_one()) {
+      bool ok = n_it > 0 && wait1(b.own, 0);
       auto slot_of = [&](int i, int u) { return (2 * i + u) % C::kRing; };
       // S = Q K^T (u = 0) or dP = dO V^T (u = 1) of block i.
       auto issue_sd = [&](int i, int u) -> bool {
         const int slot = slot_of(i, u);
         if (!wait1(&b.rfull[slot], (2 * i + u) / C::kRing)) return false;
         tc_fence_after();
-        const uint32_t ab = smem_u32(u ? sG : sQ), bb = smem_u32(sR + slot * C::kTileBytes);
+        const uint64_t da = smem_desc_sw128(smem_u32(u ? sG : sQ), 16, 1024);
+        const uint64_t db = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), 16, 1024);
         const uint32_t d = tmem + (u ? kDP : kS + (i & 1) * 128);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
-          mma_f16(d, smem_desc_sw128(ab + off, 16, 1024), smem_desc_sw128(bb + off, 16, 1024), C::kIdescS,
-                  kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) / 16;
+          mma_f16(d, da + off, db + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
         if (u) mma_commit(&b.rempty[slot]);
         mma_commit(u ? b.dpfull : &b.sfull[i & 1]);
@@ -527,16 +572,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (i + 1 < n_it && !(ok = issue_sd(i + 1, 1))) break;
         const int slot = slot_of(i, 0);
-        const uint32_t bb = smem_u32(sR + slot * C::kTileBytes);
+        const uint64_t db = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + (kk / 4) * 64 + (kk % 4) * 8,
-                     smem_desc_sw128(bb + kk * 2048, kTile * 128, 1024), C::kIdescG, (i > 0 || kk > 0) ? 1u : 0u);
+          mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + (kk / 4) * 64 + (kk % 4) * 8, db + kk * 128, C::kIdescG,
+                     (i > 0 || kk > 0) ? 1u : 0u);
         mma_commit(&b.rempty[slot]);
       }
       if (ok) mma_commit(b.done);
+      mma_commit(b.drain);
     }
-    if (lane == 0) mma_commit(b.drain);
   } else {
     // ---------------- elementwise: query row per thread, 64 key columns
     const int half = (warp - 2) / 4;
@@ -554,15 +599,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t sa = tmem + lane_off + kS + (i & 1) * 128 + half * 64, da = tmem + lane_off + kDP + half * 64;
       if (!(ok = warp_wait(&b.sfull[i & 1], i / 2))) break;
       tc_fence_after();
-      const int end = k0 + kTile > min_lim ? lim - k0 - half * 64 : 64;
-      float p[64];
+      const bool full = k0 + kTile <= min_lim;
+      const int end = lim - k0 - half * 64;
+      const float2 sl2 = make_float2(a.sl, a.sl), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
+      float2 p[32];
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
         uint32_t v[32];
         seq::tmem_ld32(sa + c2 * 32, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) p[c2 * 32 + k] = seq::ex2_approx(fmaf(__uint_as_float(v[k]), a.sl, -st.x));
+        for (int k = 0; k < 16; ++k) {
+          const float2 x =
+              __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2, nl2);
+          p[c2 * 16 + k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
+        }
       }
       if (!(ok = warp_wait(b.dpfull, i))) break;
       tc_fence_after();
@@ -573,12 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int c = c2 * 32 + 2 * k;
-          float d0 = p[c] * (__uint_as_float(v[2 * k]) - st.y);
-          float d1 = p[c + 1] * (__uint_as_float(v[2 * k + 1]) - st.y);
-          d0 = c < end ? d0 : 0.f;
-          d1 = c + 1 < end ? d1 : 0.f;
-          w[k] = seq::pack_bf16(d0, d1);
+          const float2 x = __fmul2_rn(
+              p[c2 * 16 + k],
+              __fadd2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), nd2));
+          w[k] = seq::pack_bf16(x.x, x.y);
+        }
+        if (!full) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int c = c2 * 32 + 2 * k;
+            w[k] = (c < end ? w[k] & 0xffffu : 0u) | (c + 1 < end ? w[k] & 0xffff0000u : 0u);
+          }
         }
         tmem_st16(sa + c2 * 16, w);
       }
@@ -618,11 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (*b.abort_flag && threadIdx.x == 0) {
-    if (own_issued) mbar_wait(b.own, 0, nullptr, a.status, a.wait_ns);
-    for (int i = max(0, issued - C::kRing); i < issued; ++i)
-      mbar_wait(&b.rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
-  }
   if (warp == 1) {
     if (lane == 0) mbar_wait(b.drain, 0, nullptr, a.status, a.wait_ns);
     __syncwarp();
@@ -646,7 +697,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   a.dK = static_cast<__nv_bfloat16*>(dK);
   a.dV = static_cast<__nv_bfloat16*>(dV);
   a.status = status;
-  a.wait_ns = 2000000000ull;
+  a.wait_ns = 2000000000u;
   cudaError_t e;
   const long long k_items = ((long long)c.Tk / kTile + c.N) * c.Hkv;
   const long long q_items = ((long long)c.Tq / a.tpt + c.N) * c.Hkv;
@@ -674,7 +725,8 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   if ((e = make_tmap_bf16(&mK, kp, 3, kdims, kstr, kbox)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&mV, vp, 3, kdims, vstr, kbox)) != cudaSuccess) return e;
   if (rows > 0) {
-    attn_rowdot_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(
+    const int per = 256 / (D / 8) * 4;
+    attn_rowdot_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(
         static_cast<const __nv_bfloat16*>(O), static_cast<const __nv_bfloat16*>(dO), c.o_row, lse,
         static_cast<float2*>(ws), c.Tq, c.Hq, a.G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -45,7 +45,7 @@ namespace vda {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;  // TMA warp, MMA warp, two streams of four softmax warps
+constexpr int kThreads = 384;  // TMA warp, MMA warp, two idle ones, two streams of four softmax warps
 constexpr int kMinSplitBlocks = 4;
 
 template <int D>
@@ -76,7 +76,7 @@ struct CaArgs {
   float* part_o;       // split form: [2 nsplit][Tq * Hq][D]
   float* part_l;       // split form: [2 nsplit][Tq * Hq], log2 domain
   uint32_t* status;
-  unsigned long long wait_ns;
+  uint32_t wait_ns;
 };
 
 // Keys of sequence i: first token and count (k_len, where given, is the filled
@@ -183,120 +183,131 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int issued = 0;        // ring copies issued (producer only)
-  bool q_issued = false;
 
-  if (warp == 0) {
-    // ---------------- TMA producer. Ring order is the order in which the MMA
-    // warp takes blocks: K0 (K1 in the split form, one per stream), then V_t and
-    // the next K in turn.
-    if (lane == 0 && nb_all > 0) {
-      const uint32_t q_bytes = (uint32_t)(a.tpt * a.G) * 128u;
-      const int tiles = (!kSplit && nb[1] > 0) ? 2 : 1;
-      mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * tiles);
-      for (int s = 0; s < tiles; ++s)
+  // 384 threads start with 168 registers each; the first four warps give most of
+  // theirs to the rows' 128 logits (56 + 2 x 224 = 504 = 3 x 168).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ---------------- TMA producer. Ring order is the order in which the MMA
+      // warp takes blocks: K0 (K1 in the split form, one per stream), then V_t and
+      // the next K in turn.
+      if (nb_all > 0 && seq::elect_one()) {
+        const uint32_t q_bytes = (uint32_t)(a.tpt * a.G) * 128u;
+        const int tiles = (!kSplit && nb[1] > 0) ? 2 : 1;
+        mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * tiles);
+        for (int s = 0; s < tiles; ++s)
 #pragma unroll
-        for (int at = 0; at < C::kAtoms; ++at)
-          tma_load_3d(sQ + s * C::kTileBytes + at * (kTile * 128), &mQ, qfull, at * 64, hk * a.G, q_lo + t0[s]);
-      q_issued = true;
-      auto load = [&](const CUtensorMap* m, int blk) -> bool {
-        const int slot = issued % C::kRing;
-        if (!mbar_wait(&rempty[slot], ((issued / C::kRing) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) return false;
-        mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_3d(sQ + s * C::kTileBytes + at * (kTile * 128), &mQ, qfull, at * 64, hk * a.G, q_lo + t0[s]);
+        int issued = 0;  // ring copies
+        auto load = [&](const CUtensorMap* m, int blk) -> bool {
+          const int slot = issued % C::kRing;
+          if (!seq::bar_wait(&rempty[slot], ((issued / C::kRing) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) return false;
+          mbar_arrive_expect_tx(&rfull[slot], C::kTileBytes);
 #pragma unroll
-        for (int at = 0; at < C::kAtoms; ++at)
-          tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), m, &rfull[slot], at * 64, hk,
-                      k_lo + (b_lo + blk) * kTile);
-        ++issued;
-        return true;
-      };
-      constexpr int ahead = kSplit ? 2 : 1;
-      bool ok = load(&mK, 0);
-      if (kSplit && ok && nb_all > 1) ok = load(&mK, 1);
-      for (int t = 0; t < nb_all && ok; ++t) {
-        ok = load(&mV, t);
-        if (ok && t + ahead < nb_all) ok = load(&mK, t + ahead);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer. Products of one thread run in issue order, so
-    // the next S of a stream, issued after P V of the last, cannot overwrite the
-    // probabilities that product reads.
-    if (lane == 0) {
-      bool ok = nb_all == 0 || mbar_wait(qfull, 0, abort_flag, a.status, a.wait_ns);
-      int taken = 0;  // ring position
-      auto take = [&](int& slot) -> bool {
-        slot = taken % C::kRing;
-        const bool r = mbar_wait(&rfull[slot], (taken / C::kRing) & 1, abort_flag, a.status, a.wait_ns);
-        ++taken;
-        return r;
-      };
-      auto issue_s = [&](int s, int slot) {
-        const uint32_t qb = smem_u32(sQ + (kSplit ? 0 : s) * C::kTileBytes);
-        const uint32_t kb = smem_u32(sR + slot * C::kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
-          mma_f16(tmem + (s ? C::kS1 : C::kS0), smem_desc_sw128(qb + off, 16, 1024),
-                  smem_desc_sw128(kb + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), m, &rfull[slot], at * 64, hk,
+                        k_lo + (b_lo + blk) * kTile);
+          ++issued;
+          return true;
+        };
+        constexpr int ahead = kSplit ? 2 : 1;
+        bool ok = load(&mK, 0);
+        if (kSplit && ok && nb_all > 1) ok = load(&mK, 1);
+        for (int t = 0; t < nb_all && ok; ++t) {
+          ok = load(&mV, t);
+          if (ok && t + ahead < nb_all) ok = load(&mK, t + ahead);
         }
-        mma_commit(&sfull[s]);
-      };
-      auto issue_pv = [&](int s, int j, int slot) -> bool {
-        if (!mbar_wait(&pfull[s], j & 1, abort_flag, a.status, a.wait_ns)) return false;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sR + slot * C::kTileBytes);
+        if (*abort_flag) {
+          // Let every issued copy land before the CTA's shared memory is released.
+          mbar_wait(qfull, 0, nullptr, a.status, a.wait_ns);
+          for (int i = max(0, issued - C::kRing); i < issued; ++i)
+            mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------- MMA issuer. Products of one thread run in issue order, so
+      // the next S of a stream, issued after P V of the last, cannot overwrite the
+      // probabilities that product reads.
+      if (seq::elect_one()) {
+        bool ok = nb_all == 0 || seq::bar_wait(qfull, 0, abort_flag, a.status, a.wait_ns);
+        int taken = 0;  // ring position
+        auto take = [&](int& slot) -> bool {
+          slot = taken % C::kRing;
+          const bool r = seq::bar_wait(&rfull[slot], (taken / C::kRing) & 1, abort_flag, a.status, a.wait_ns);
+          ++taken;
+          return r;
+        };
+        auto issue_s = [&](int s, int slot) {
+          // The address field of a descriptor counts 16 bytes: steps are added to it.
+          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + (kSplit ? 0 : s) * C::kTileBytes), 16, 1024);
+          const uint64_t dk = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8,
-                     smem_desc_sw128(vb + kk * 2048, kTile * 128, 1024), C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&pvdone[s]);
-        return true;
-      };
-      int slot = 0, vslot = 0;
-      if (ok && nb_all > 0) {
-        if (kSplit) {
-          for (int s = 0; s < min(2, nb_all) && ok; ++s) {
-            if (!(ok = take(slot))) break;
-            issue_s(s, slot);
-            mma_commit(&rempty[slot]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) / 16;
+            mma_f16(tmem + (s ? C::kS1 : C::kS0), dq + off, dk + off, C::kIdescS, kk > 0 ? 1u : 0u);
           }
-          for (int t = 0; t < nb_all && ok; ++t) {
-            if (!(ok = take(vslot)) || !(ok = issue_pv(t & 1, t >> 1, vslot))) break;
-            mma_commit(&rempty[vslot]);
-            if (t + 2 < nb_all) {
+          mma_commit(&sfull[s]);
+        };
+        auto issue_pv = [&](int s, int j, int slot) -> bool {
+          if (!seq::bar_wait(&pfull[s], j & 1, abort_flag, a.status, a.wait_ns)) return false;
+          tc_fence_after();
+          const uint64_t dv = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), kTile * 128, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8, dv + kk * 128, C::kIdescO,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&pvdone[s]);
+          return true;
+        };
+        int slot = 0, vslot = 0;
+        if (ok && nb_all > 0) {
+          if (kSplit) {
+            for (int s = 0; s < min(2, nb_all) && ok; ++s) {
               if (!(ok = take(slot))) break;
-              issue_s(t & 1, slot);
+              issue_s(s, slot);
               mma_commit(&rempty[slot]);
             }
-          }
-        } else {
-          if ((ok = take(slot))) {
-            for (int s = 0; s < 2; ++s)
-              if (nb[s] > 0) issue_s(s, slot);
-            mma_commit(&rempty[slot]);
-          }
-          for (int i = 0; i < nb_all && ok; ++i) {
-            if (!(ok = take(vslot))) break;
-            bool have = false;
-            for (int s = 0; s < 2 && ok; ++s) {
-              if (i < nb[s] && !(ok = issue_pv(s, i, vslot))) break;
-              if (s == 1) mma_commit(&rempty[vslot]);
-              if (i + 1 < nb[s]) {
-                if (!have && !(ok = take(slot))) break;
-                have = true;
-                issue_s(s, slot);
+            for (int t = 0; t < nb_all && ok; ++t) {
+              if (!(ok = take(vslot)) || !(ok = issue_pv(t & 1, t >> 1, vslot))) break;
+              mma_commit(&rempty[vslot]);
+              if (t + 2 < nb_all) {
+                if (!(ok = take(slot))) break;
+                issue_s(t & 1, slot);
+                mma_commit(&rempty[slot]);
               }
             }
-            if (ok && have) mma_commit(&rempty[slot]);
+          } else {
+            if ((ok = take(slot))) {
+              for (int s = 0; s < 2; ++s)
+                if (nb[s] > 0) issue_s(s, slot);
+              mma_commit(&rempty[slot]);
+            }
+            for (int i = 0; i < nb_all && ok; ++i) {
+              if (!(ok = take(vslot))) break;
+              bool have = false;
+              for (int s = 0; s < 2 && ok; ++s) {
+                if (i < nb[s] && !(ok = issue_pv(s, i, vslot))) break;
+                if (s == 1) mma_commit(&rempty[vslot]);
+                if (i + 1 < nb[s]) {
+                  if (!have && !(ok = take(slot))) break;
+                  have = true;
+                  issue_s(s, slot);
+                }
+              }
+              if (ok && have) mma_commit(&rempty[slot]);
+            }
           }
         }
+        mma_commit(drain);
       }
-      mma_commit(drain);
     }
+    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---------------- softmax and epilogue: stream s, one row per thread
-    const int s = (warp - 2) / 4;
+    const int s = (warp - 4) / 4;
     const int quad = warp % 4;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool w = mbar_wait(bar, parity, abort_flag, a.status, a.wait_ns);
+      const bool w = seq::bar_wait(bar, parity, abort_flag, a.status, a.wait_ns);
       return __all_sync(0xffffffffu, w);
     };
     for (int j = 0; j < my_nb; ++j) {
@@ -460,12 +471,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && threadIdx.x == 0) {
-    // Let every issued copy land before the CTA's shared memory is released.
-    if (q_issued) mbar_wait(qfull, 0, nullptr, a.status, a.wait_ns);
-    for (int i = max(0, issued - C::kRing); i < issued; ++i)
-      mbar_wait(&rfull[i % C::kRing], (i / C::kRing) & 1, nullptr, a.status, a.wait_ns);
-  }
   if (warp == 1) {
     if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
     __syncwarp();
@@ -570,7 +575,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
     a.part_l = a.part_o + 2LL * p.nsplit * rows * D;
   }
   a.status = status;
-  a.wait_ns = 2000000000ull;
+  a.wait_ns = 2000000000u;
   const int per_item = p.split ? a.tpt : 2 * a.tpt;
   // ceil(n / per_item) summed over the sequences is at most Tq / per_item + N.
   const long long items = (long long)c.Tq / per_item + c.N;

@@ -107,7 +107,7 @@ struct DaArgs {
   DaJob job[kMaxJobs];
   float* seg_state;         // [items][H][njobs][d * d]
   uint32_t* status;
-  unsigned long long wait_ns;
+  uint32_t wait_ns;
 };
 
 // a^e for the head's log2 decay g2 (finite, see head_decay).
@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
   int loaded = 0;  // chunks whose copies have been issued
   auto wait1 = [&](uint64_t* bar, uint32_t n) -> bool {  // n-th phase of the barrier, n = 0, 1, ...
-    return seq::bar_wait(bar, n & 1, abort_flag, a.status, (uint32_t)a.wait_ns);
+    return seq::bar_wait(bar, n & 1, abort_flag, a.status, a.wait_ns);
   };
   auto warp_wait = [&](uint64_t* bar, uint32_t n) -> bool {
-    return seq::warp_wait(bar, n & 1, abort_flag, a.status, (uint32_t)a.wait_ns);
+    return seq::warp_wait(bar, n & 1, abort_flag, a.status, a.wait_ns);
   };
 
   // One step of V' by a group of four warps: its 32 tokens, 32 value channels (TMEM
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
           // Let every issued copy land before the CTA's shared memory is released.
           for (int i = max(0, loaded - 6); i < loaded; ++i)
             if (!kStateOnly || i % 3 != 0)
-              mbar_wait(&rfull[slot_of(i / 3, i % 3)], (i / 6) & 1, nullptr, a.status, (uint32_t)a.wait_ns);
+              mbar_wait(&rfull[slot_of(i / 3, i % 3)], (i / 6) & 1, nullptr, a.status, a.wait_ns);
         }
       }
     } else if (warp == 1) {
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   if (warp == 3) {
-    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, (uint32_t)a.wait_ns);
+    if (lane == 0) mbar_wait(drain, 0, nullptr, a.status, a.wait_ns);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -861,7 +861,7 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
   const bool whole = (long long)c.T <= (long long)a.seg * kC;  // no sequence can be longer than a segment
   const long long items = segment_items(c, a.seg);
   a.seg_state = whole ? nullptr : static_cast<float*>(ws);
-  a.wait_ns = 2000000000ull;
+  a.wait_ns = 2000000000u;
   const long long grid = items * c.H * a.njobs;
   if (grid >= (1LL << 31) || c.N > 65535) return cudaErrorInvalidConfiguration;
   DaMaps maps{};
