@@ -17,8 +17,9 @@
 //   bf16 back into the TMEM columns they came from, dV += P^T dO_i,
 //   dK += dS^T Q_i (left operands from TMEM). S and dP of the next tile are issued
 //   as soon as the product that reads their columns is, so tensor cores and
-//   exponentials overlap. Eight warps share the elementwise work, half the
-//   columns each.
+//   exponentials overlap. Sixteen warps share the elementwise work, a quarter of
+//   the columns each (with eight, a tile's two elementwise phases took 3460 of its
+//   4360 cycles).
 // Third launch, per key block i (rows = queries): S = Q K_i^T into one of two
 //   buffers, dP = dO V_i^T, dS as bf16 over S, dQ += dS K_i.
 //
@@ -39,7 +40,7 @@ namespace vda {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;  // TMA warp, MMA warp, eight elementwise warps
+constexpr int kThreads = 576;  // TMA warp, MMA warp, sixteen elementwise warps
 
 template <int D>
 struct CbCfg {
@@ -150,11 +151,11 @@ struct CbBars {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&stfull[i], 1);
-      mbar_init(&stempty[i], 8);
+      mbar_init(&stempty[i], 16);
     }
-    mbar_init(pfull, 8);
+    mbar_init(pfull, 16);
     mbar_init(dpfull, 1);
-    mbar_init(dsfull, 8);
+    mbar_init(dsfull, 16);
     mbar_init(done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -164,8 +165,8 @@ struct CbBars {
 
 // ---------------------------------------------------------------- dK and dV
 // TMEM: S^T | dP^T | dV | dK. Query column c of P^T (dS^T) lies, packed, at
-// column (c % 64) / 2 + (c / 64) * 64 of S^T (dP^T): each half of the elementwise
-// warps overwrites only columns that it has read itself.
+// column (c % 32) / 2 + (c / 32) * 32 of S^T (dP^T): each quarter of the
+// elementwise warps overwrites only columns that it has read itself.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = u * 32 + lane;
-          const float2 v = r < live ? src[r] : make_float2(0.f, 0.f);
+          const float2 v = r < live ? src[r] : make_float2(INFINITY, 0.f);  // a row that is none weighs 0
           stat[(i & 1) * 2 * kTile + r] = -v.x;
           stat[(i & 1) * 2 * kTile + kTile + r] = -v.y;
         }
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t db = smem_desc_sw128(smem_u32(sR + slot_of(i, 1 - u) * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + (u ? kDK : kDV), tmem + (u ? kDP : kS) + (kk / 4) * 64 + (kk % 4) * 8, db + kk * 128,
+          mma_f16_ts(tmem + (u ? kDK : kDV), tmem + (u ? kDP : kS) + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128,
                      C::kIdescG, (i > 0 || kk > 0) ? 1u : 0u);
         return true;
       };
@@ -324,60 +325,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(b.drain);
     }
   } else {
-    // ---------------- elementwise: key row per thread, 64 query columns
-    const int half = (warp - 2) / 4;
+    // ---------------- elementwise: key row per thread, 32 query columns
+    const int part = (warp - 2) / 4;
     const int quad = warp % 4;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t sa = tmem + lane_off + kS + half * 64, da = tmem + lane_off + kDP + half * 64;
+    const uint32_t sa = tmem + lane_off + kS + part * 32, da = tmem + lane_off + kDP + part * 32;
     const int key = k0 + r;
+    const float2 sl2 = make_float2(a.sl, a.sl);
     bool ok = true;
     for (int i = 0; i < n_it; ++i) {
       const int t0 = (i0 + i) * a.tpt;
       const bool ragged = t0 + a.tpt > nq;
-      // Every key of the block is seen by every row of the tile, and every column is a row.
-      const bool full = !ragged && rows == kTile && shift + t0 >= k0 + kTile - 1;
+      // Every key of the block is seen by every row of the tile. (Where 128 is not a
+      // multiple of G, the columns that are no rows are zero in Q and dO.)
+      const bool full = !ragged && shift + t0 >= k0 + kTile - 1;
+      // Else this row's key is seen by columns first .. end - 1 (token >= key - shift).
+      const int first = max(0, (key - shift - t0)) * a.G - part * 32;
+      const int end = min(a.tpt, nq - t0) * a.G - part * 32;
+      auto mask = [&](uint32_t (&w)[16]) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int c = 2 * k;
+          w[k] = (c >= first && c < end ? w[k] & 0xffffu : 0u) |
+                 (c + 1 >= first && c + 1 < end ? w[k] & 0xffff0000u : 0u);
+        }
+      };
       if (!(ok = warp_wait(&b.stfull[i & 1], i / 2))) break;
       if (!(ok = warp_wait(&b.sfull[0], i))) break;
       tc_fence_after();
-      const float* st = stat + (i & 1) * 2 * kTile + half * 64;
-      float2 p[32];
-      // First column that sees this row's key: token >= key - shift.
-      const int first = max(0, (key - shift - t0)) * a.G - half * 64;
-      const int end = min(a.tpt, nq - t0) * a.G - half * 64;
-      auto mask = [&](int c, uint32_t w) -> uint32_t {  // columns c, c + 1
-        return (c >= first && c < end ? w & 0xffffu : 0u) | (c + 1 >= first && c + 1 < end ? w & 0xffff0000u : 0u);
-      };
-      const float2 sl2 = make_float2(a.sl, a.sl);
+      const float* st = stat + (i & 1) * 2 * kTile + part * 32;
+      uint32_t v[32], w[16];
+      float2 p[16];
+      seq::tmem_ld32(sa, v);
+      tmem_ld_wait();
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t v[32], w[16];
-        seq::tmem_ld32(sa + c2 * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const float4 l = *reinterpret_cast<const float4*>(st + c2 * 32 + 2 * k);
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2,
-                                      make_float2(l.x, l.y));
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])), sl2,
-                                      make_float2(l.z, l.w));
-          p[c2 * 16 + k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
-          p[c2 * 16 + k + 1] = make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = seq::pack_bf16(p[c2 * 16 + k].x, p[c2 * 16 + k].y);
-        if (!full) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = mask(c2 * 32 + 2 * k, w[k]);
-        }
-        tmem_st16(sa + c2 * 16, w);
+      for (int k = 0; k < 16; k += 2) {
+        const float4 l = *reinterpret_cast<const float4*>(st + 2 * k);
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2,
+                                    make_float2(l.x, l.y));
+        const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])), sl2,
+                                    make_float2(l.z, l.w));
+        p[k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
+        p[k + 1] = make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
       }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = seq::pack_bf16(p[k].x, p[k].y);
+      if (!full) mask(w);
+      tmem_st16(sa, w);
       tmem_st_wait();
       if (ragged) {
-        // Query rows behind the sequence: zero them in both tiles.
+        // Query rows behind the sequence: zero them in both tiles (Q by two of the quarters, dO by the others).
         const int gs = 2 * i + 1;
         if (!(ok = warp_wait(&b.rfull[gs % C::kRing], gs / C::kRing))) break;
-        if (r >= (nq - t0) * a.G) seq::zero_row(sR + ((2 * i + half) % C::kRing) * C::kTileBytes, C::kAtoms, r, kTile);
+        if (part < 2 && r >= (nq - t0) * a.G)
+          seq::zero_row(sR + ((2 * i + part) % C::kRing) * C::kTileBytes, C::kAtoms, r, kTile);
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -385,29 +387,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(b.pfull);
       if (!(ok = warp_wait(b.dpfull, i))) break;
       tc_fence_after();
+      seq::tmem_ld32(da, v);
+      tmem_ld_wait();
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t v[32], w[16];
-        seq::tmem_ld32(da + c2 * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const float4 l = *reinterpret_cast<const float4*>(st + kTile + c2 * 32 + 2 * k);
-          const float2 x = __fmul2_rn(p[c2 * 16 + k], __fadd2_rn(make_float2(__uint_as_float(v[2 * k]),
-                                                                             __uint_as_float(v[2 * k + 1])),
-                                                                 make_float2(l.x, l.y)));
-          const float2 y = __fmul2_rn(p[c2 * 16 + k + 1], __fadd2_rn(make_float2(__uint_as_float(v[2 * k + 2]),
-                                                                                 __uint_as_float(v[2 * k + 3])),
-                                                                     make_float2(l.z, l.w)));
-          w[k] = seq::pack_bf16(x.x, x.y);
-          w[k + 1] = seq::pack_bf16(y.x, y.y);
-        }
-        if (!full) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = mask(c2 * 32 + 2 * k, w[k]);
-        }
-        tmem_st16(da + c2 * 16, w);
+      for (int k = 0; k < 16; k += 2) {
+        const float4 l = *reinterpret_cast<const float4*>(st + kTile + 2 * k);
+        const float2 x = __fmul2_rn(
+            p[k], __fadd2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(l.x, l.y)));
+        const float2 y = __fmul2_rn(p[k + 1], __fadd2_rn(make_float2(__uint_as_float(v[2 * k + 2]),
+                                                                     __uint_as_float(v[2 * k + 3])),
+                                                         make_float2(l.z, l.w)));
+        w[k] = seq::pack_bf16(x.x, x.y);
+        w[k + 1] = seq::pack_bf16(y.x, y.y);
       }
+      if (!full) mask(w);
+      tmem_st16(da, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -416,16 +410,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(b.dsfull);
       }
     }
-    // ---------------- epilogue: the first half writes dV, the second dK
+    // ---------------- epilogue: two quarters write dV, two dK, half the channels each
     if (ok && (n_it == 0 || warp_wait(b.done, 0))) {
       tc_fence_after();
       const bool live = key < nk;
-      const float f = half ? a.scale : 1.f;
-      const long long at = ((long long)(k_lo + (live ? key : k0)) * a.Hkv + hk) * D;
-      uint4* dst = reinterpret_cast<uint4*>((half ? a.dK : a.dV) + at);
-      const uint32_t ga = tmem + lane_off + (half ? kDK : kDV);
+      const bool is_k = part >= 2;
+      const int col = part % 2 * (D / 2);
+      const float f = is_k ? a.scale : 1.f;
+      const long long at = ((long long)(k_lo + (live ? key : k0)) * a.Hkv + hk) * D + col;
+      uint4* dst = reinterpret_cast<uint4*>((is_k ? a.dK : a.dV) + at);
+      const uint32_t ga = tmem + lane_off + (is_k ? kDK : kDV) + col;
 #pragma unroll
-      for (int c4 = 0; c4 < D / 32; ++c4) {
+      for (int c4 = 0; c4 < D / 64; ++c4) {
         uint32_t v[32];
         seq::tmem_ld32(ga + c4 * 32, v);
         tmem_ld_wait();
@@ -575,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t db = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + (kk / 4) * 64 + (kk % 4) * 8, db + kk * 128, C::kIdescG,
+          mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128, C::kIdescG,
                      (i > 0 || kk > 0) ? 1u : 0u);
         mma_commit(&b.rempty[slot]);
       }
@@ -583,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(b.drain);
     }
   } else {
-    // ---------------- elementwise: query row per thread, 64 key columns
-    const int half = (warp - 2) / 4;
+    // ---------------- elementwise: query row per thread, 32 key columns
+    const int part = (warp - 2) / 4;
     const int quad = warp % 4;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -593,80 +589,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lim = min(nk, shift + tok + 1);
     const int min_lim = shift + t0 + 1;
     const float2 st = live ? a.stat[((long long)hk * a.Tq + q_lo + t0) * a.G + r] : make_float2(0.f, 0.f);
+    const float2 sl2 = make_float2(a.sl, a.sl), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
     bool ok = true;
     for (int i = 0; i < n_it; ++i) {
       const int k0 = i * kTile;
-      const uint32_t sa = tmem + lane_off + kS + (i & 1) * 128 + half * 64, da = tmem + lane_off + kDP + half * 64;
+      const uint32_t sa = tmem + lane_off + kS + (i & 1) * 128 + part * 32, da = tmem + lane_off + kDP + part * 32;
       if (!(ok = warp_wait(&b.sfull[i & 1], i / 2))) break;
       tc_fence_after();
-      const bool full = k0 + kTile <= min_lim;
-      const int end = lim - k0 - half * 64;
-      const float2 sl2 = make_float2(a.sl, a.sl), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
-      float2 p[32];
+      uint32_t v[32], w[16];
+      float2 p[16];
+      seq::tmem_ld32(sa, v);
+      tmem_ld_wait();
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t v[32];
-        seq::tmem_ld32(sa + c2 * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 x =
-              __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2, nl2);
-          p[c2 * 16 + k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
-        }
+      for (int k = 0; k < 16; ++k) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2, nl2);
+        p[k] = make_float2(seq::ex2_approx(x.x), seq::ex2_approx(x.y));
       }
       if (!(ok = warp_wait(b.dpfull, i))) break;
       tc_fence_after();
+      seq::tmem_ld32(da, v);
+      tmem_ld_wait();
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t v[32], w[16];
-        seq::tmem_ld32(da + c2 * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 x = __fmul2_rn(
-              p[c2 * 16 + k],
-              __fadd2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), nd2));
-          w[k] = seq::pack_bf16(x.x, x.y);
-        }
-        if (!full) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int c = c2 * 32 + 2 * k;
-            w[k] = (c < end ? w[k] & 0xffffu : 0u) | (c + 1 < end ? w[k] & 0xffff0000u : 0u);
-          }
-        }
-        tmem_st16(sa + c2 * 16, w);
+      for (int k = 0; k < 16; ++k) {
+        const float2 x = __fmul2_rn(
+            p[k], __fadd2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), nd2));
+        w[k] = seq::pack_bf16(x.x, x.y);
       }
+      if (k0 + kTile > min_lim) {
+        const int end = lim - k0 - part * 32;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          w[k] = (2 * k < end ? w[k] & 0xffffu : 0u) | (2 * k + 1 < end ? w[k] & 0xffff0000u : 0u);
+      }
+      tmem_st16(sa, w);
       tmem_st_wait();
       if (k0 + kTile > nk) {
-        if (half == 0 && k0 + r >= nk) seq::zero_row(sR + ((2 * i) % C::kRing) * C::kTileBytes, C::kAtoms, r, kTile);
+        // Key rows behind the sequence are summed over: zero them.
+        if (part == 0 && k0 + r >= nk) seq::zero_row(sR + ((2 * i) % C::kRing) * C::kTileBytes, C::kAtoms, r, kTile);
         fence_proxy_async_smem();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b.dsfull);
     }
-    // ---------------- epilogue: half the channels each
+    // ---------------- epilogue: a quarter of the channels each
     if (ok && (n_it == 0 || warp_wait(b.done, 0))) {
       tc_fence_after();
+      constexpr int kCols = D / 4;
       const long long at = ((long long)(q_lo + (live ? tok : t0)) * (a.Hkv * a.G) + hk * a.G + r % a.G) * D;
-      uint4* dst = reinterpret_cast<uint4*>(a.dQ + at + half * (D / 2));
+      uint4* dst = reinterpret_cast<uint4*>(a.dQ + at + part * kCols);
 #pragma unroll
-      for (int c4 = 0; c4 < D / 64; ++c4) {
-        uint32_t v[32];
-        seq::tmem_ld32(tmem + lane_off + kDQ + half * (D / 2) + c4 * 32, v);
+      for (int c = 0; c < kCols / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lane_off + kDQ + part * kCols + c * 16, v);
         tmem_ld_wait();
         if (!live) continue;
 #pragma unroll
-        for (int q8 = 0; q8 < 4; ++q8) {
+        for (int q8 = 0; q8 < 2; ++q8) {
           uint32_t op[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             op[k] = n_it > 0 ? seq::pack_bf16(__uint_as_float(v[q8 * 8 + 2 * k]) * a.scale,
                                               __uint_as_float(v[q8 * 8 + 2 * k + 1]) * a.scale)
                              : 0u;
-          dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
+          dst[c * 2 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
         }
       }
     }
