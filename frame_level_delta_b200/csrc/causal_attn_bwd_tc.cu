@@ -46,11 +46,11 @@ template <int D>
 struct CbCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kRing = D == 128 ? 4 : 8;  // tiles in flight
+  static constexpr int kRing = D == 128 ? 5 : 8;  // tiles in flight
   static constexpr int kRingOff = 2 * kTileBytes;  // behind the CTA's own two tiles (K, V or Q, dO)
   static constexpr int kStatOff = kRingOff + kRing * kTileBytes;  // two stages of 128 (lse2, D)
   static constexpr int kBarOff = kStatOff + 2 * kTile * 8;
-  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static constexpr int kSmemBytes = kBarOff + 512;  // the array is declared 1024-byte aligned: no room to align it
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescG = sm100::idesc_bf16_f32(128, D, false, true);
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = CbCfg<D>;
   using namespace sm100;
   constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 256 + D;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  uint8_t* smem = smem_1024;
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTileBytes;
   uint8_t* sR = smem + C::kRingOff;
@@ -315,10 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && issue_sd(0, 0) && issue_sd(0, 1);
       for (int i = 0; i < n_it && ok; ++i) {
         if (!(ok = issue_g(i, 0))) break;
+        mma_commit(&b.rempty[slot_of(i, 1)]);  // dO: read by dP and dV
         if (i + 1 < n_it && !(ok = issue_sd(i + 1, 0))) break;
         if (!(ok = issue_g(i, 1))) break;
-        mma_commit(&b.rempty[slot_of(i, 0)]);
-        mma_commit(&b.rempty[slot_of(i, 1)]);
+        mma_commit(&b.rempty[slot_of(i, 0)]);  // Q: read by S and dK
         if (i + 1 < n_it && !(ok = issue_sd(i + 1, 1))) break;
       }
       if (ok) mma_commit(b.done);
@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = CbCfg<D>;
   using namespace sm100;
   constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  uint8_t* smem = smem_1024;
   uint8_t* sQ = smem;
   uint8_t* sG = smem + C::kTileBytes;
   uint8_t* sR = smem + C::kRingOff;
