@@ -614,43 +614,59 @@ def _cuda_device(t) -> torch.device:
     return t.device
 
 
-class _On:
-    """The device and stream of a call: what is allocated inside belongs to the stream it is used on."""
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-
-    def __enter__(self):
-        self.guard = None
-        if self.stream is not None:
-            if self.stream.device != self.dev:
-                raise ValueError(f"the stream is on {self.stream.device}; the tensors are on {self.dev}")
-            self.guard = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-        if self.guard is not None:
-            self.guard.__enter__()
-        return ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+# Checked calls by what was checked: shapes, strides, types and devices of every
+# argument (never an address). A program makes the same call over and over, and the
+# checks would cost more than the launch.
+_checked: Dict[tuple, tuple] = {}
 
 
-def _workspace(what: str, cfg, dev) -> Tuple[Optional[torch.Tensor], int]:
+def _signature(*tensors) -> tuple:
+    try:
+        return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
+    except AttributeError:
+        return ()  # something that is no tensor: checked, and refused, every time
+
+
+def _remember(key: tuple, value: tuple) -> tuple:
+    if len(_checked) >= 4096:
+        _checked.clear()
+    if key:
+        _checked[key] = value
+    return value
+
+
+def _workspace_bytes(what: str, cfg) -> int:
     n = ctypes.c_size_t(0)
     st = getattr(lib(), what)(ctypes.byref(cfg), ctypes.byref(n))
     if st != VDA_OK:
         raise VDAError(st, what)
-    if n.value == 0:
-        return None, 0
-    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+    return n.value
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(what: str, dev, stream, make):
+    """Call ``what`` on the tensors' device and the given (or current) stream.
+    ``make`` allocates what the call needs and returns the C arguments; it runs with
+    that stream current, so what it allocates belongs to the stream it is used on."""
+    # The current device and stream as the runtime's own calls give them: through
+    # torch.cuda's objects the two cost half of a small call's time.
+    if stream is None and torch._C._cuda_getDevice() == dev.index:
+        st = getattr(_lib or lib(), what)(*make(), torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}; the tensors are on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):  # stream None: the device's current one
+            st = getattr(lib(), what)(*make(), torch.cuda.current_stream().cuda_stream)
+    if st != VDA_OK:
+        raise VDAError(st, what)
 
 
 def _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev) -> vda_attention_config:
     N = _starts("cu_q", cu_q, dev)
-    if cu_k is not cu_q and _starts("cu_k", cu_k, dev) != N:
+    if _starts("cu_k", cu_k, dev) != N:
         raise ValueError("cu_q and cu_k hold different numbers of sequences")
     _flat("k_len", k_len, (N,), torch.int32, dev)
     q_row = _rows("Q", Q, (None, None, None), dev)
@@ -661,10 +677,16 @@ def _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev) -> vda_attentio
     o_row = Hq * d if O is None else _rows("O", O, (Tq, Hq, d), dev)
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads are no multiple of {Hkv} key heads")
-    if cu_k is cu_q and Tk != Tq:
-        raise ValueError(f"K has {Tk} tokens and Q {Tq}: give cu_k where keys and queries are not the same tokens")
     return vda_attention_config(N, Hq, Hkv, d, Tq, Tk, q_row, k_row, v_row, o_row,
                                 d ** -0.5 if scale is None else scale)
+
+
+def _check_attention(Q, K, V, cu_q, cu_k, k_len, scale, O):
+    dev = _cuda_device(Q)
+    c = _attention_config(Q, K, V, O, cu_q, cu_q if cu_k is None else cu_k, k_len, scale, dev)
+    if cu_k is None and c.Tk != c.Tq:
+        raise ValueError(f"K has {c.Tk} tokens and Q {c.Tq}: give cu_k where keys and queries are not the same tokens")
+    return c, dev, _workspace_bytes("vda_causal_attention_workspace", c)
 
 
 def causal_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
@@ -677,20 +699,38 @@ def causal_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: to
     against a cache (cu_k: the caches' rooms, k_len: their filled parts) is a step
     of generation. ``scale`` defaults to 1 / sqrt(d). Returns O, or (O, lse) with
     lse [Tq, Hq] float32."""
-    dev = _cuda_device(Q)
-    if cu_k is None:
-        cu_k = cu_q
-    c = _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev)
-    with _On(dev, stream) as s:
-        ws, n = _workspace("vda_causal_attention_workspace", c, dev)
+    key = _signature(Q, K, V, cu_q, cu_k, k_len, O)
+    key = key and ("attention", key, scale)
+    c, dev, n = _checked.get(key) or _remember(key, _check_attention(Q, K, V, cu_q, cu_k, k_len, scale, O))
+    lse = None
+
+    def make():
+        nonlocal O, lse
+        ws = Q.new_empty(n, dtype=torch.uint8) if n else None
         if O is None:
-            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
-        lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
-        st = lib().vda_causal_attention(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(cu_q), _ptr(cu_k),
-                                        _ptr(k_len), _ptr(O), _ptr(lse), _ptr(ws), n, s)
-    if st != VDA_OK:
-        raise VDAError(st, "vda_causal_attention")
+            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        if return_lse:
+            lse = Q.new_empty(Q.shape[:2], dtype=torch.float32)
+        return (ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), cu_q.data_ptr(),
+                (cu_q if cu_k is None else cu_k).data_ptr(), _addr(k_len), O.data_ptr(), _addr(lse), _addr(ws), n)
+
+    _run("vda_causal_attention", dev, stream, make)
     return (O, lse) if return_lse else O
+
+
+def _check_attention_backward(Q, K, V, O, dO, lse, cu_q, cu_k, k_len, scale, out):
+    c, dev, _ = _check_attention(Q, K, V, cu_q, cu_k, k_len, scale, O)
+    if O is None or dO is None or lse is None:
+        raise ValueError("O, dO and lse are required")
+    if _rows("dO", dO, tuple(O.shape), dev) != c.o_row and O.shape[0] > 1:
+        raise ValueError("O and dO must have the same distance between tokens")
+    _flat("lse", lse, tuple(Q.shape[:2]), torch.float32, dev)
+    if out is not None:
+        for k, t, g in (("dQ", Q, out[0]), ("dK", K, out[1]), ("dV", V, out[2])):
+            if g is None:
+                raise ValueError(f"out must hold {k}")
+            _flat(k, g, tuple(t.shape), torch.bfloat16, dev)
+    return c, dev, _workspace_bytes("vda_causal_attention_backward_workspace", c)
 
 
 def causal_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
@@ -701,24 +741,23 @@ def causal_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
     """Gradients of causal_attention (vda_causal_attention_backward) from the O and
     lse it returned: dQ, dK, dV (bf16, contiguous). Rows outside the sequences are
     not written: uninitialised in tensors made here, as they were in ``out``."""
-    dev = _cuda_device(Q)
-    if cu_k is None:
-        cu_k = cu_q
-    c = _attention_config(Q, K, V, O, cu_q, cu_k, k_len, scale, dev)
-    if _rows("dO", dO, tuple(O.shape), dev) != c.o_row and O.shape[0] > 1:
-        raise ValueError("O and dO must have the same distance between tokens")
-    _flat("lse", lse, tuple(Q.shape[:2]), torch.float32, dev)
-    with _On(dev, stream) as s:
-        ws, n = _workspace("vda_causal_attention_backward_workspace", c, dev)
+    given = None if out is None else (out.get("dQ"), out.get("dK"), out.get("dV"))
+    key = _signature(Q, K, V, O, dO, lse, cu_q, cu_k, k_len, *(given or ()))
+    key = key and ("attention backward", key, scale)
+    c, dev, n = _checked.get(key) or _remember(
+        key, _check_attention_backward(Q, K, V, O, dO, lse, cu_q, cu_k, k_len, scale, given))
+
+    def make():
+        nonlocal out
+        ws = Q.new_empty(n, dtype=torch.uint8)
         if out is None:
-            out = {k: torch.empty(t.shape, dtype=t.dtype, device=dev) for k, t in (("dQ", Q), ("dK", K), ("dV", V))}
-        for k, t in (("dQ", Q), ("dK", K), ("dV", V)):
-            _flat(k, out[k], tuple(t.shape), torch.bfloat16, dev)
-        st = lib().vda_causal_attention_backward(
-            ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
-            _ptr(k_len), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(ws), n, s)
-    if st != VDA_OK:
-        raise VDAError(st, "vda_causal_attention_backward")
+            out = {k: torch.empty_like(t, memory_format=torch.contiguous_format)
+                   for k, t in (("dQ", Q), ("dK", K), ("dV", V))}
+        return (ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(),
+                lse.data_ptr(), cu_q.data_ptr(), (cu_q if cu_k is None else cu_k).data_ptr(), _addr(k_len),
+                out["dQ"].data_ptr(), out["dK"].data_ptr(), out["dV"].data_ptr(), ws.data_ptr(), n)
+
+    _run("vda_causal_attention_backward", dev, stream, make)
     return out
 
 
@@ -728,7 +767,19 @@ def _decay_config(Q, K, V, O, log_decay, N, scale, dev, oname="O") -> vda_decay_
     k_row, v_row = _rows("K", K, (T, H, d), dev), _rows("V", V, (T, H, d), dev)
     o_row = H * d if O is None else _rows(oname, O, (T, H, d), dev)
     _flat("log_decay", log_decay, (H,), torch.float32, dev)
+    if log_decay is None:
+        raise ValueError("log_decay is required")
     return vda_decay_config(N, H, d, T, q_row, k_row, v_row, o_row, scale)
+
+
+def _check_decay(Q, K, V, log_decay, cu, S0, scale, O, S):
+    dev = _cuda_device(Q)
+    N = _starts("cu", cu, dev)
+    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
+    shape = (N, c.H, c.d, c.d)
+    _flat("S0", S0, shape, torch.float32, dev)
+    _flat("S", S, shape, torch.float32, dev)
+    return c, dev, _workspace_bytes("vda_decay_attention_workspace", c)
 
 
 def decay_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay: torch.Tensor, cu: torch.Tensor,
@@ -739,23 +790,32 @@ def decay_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay
     o_t = scale S_t q_t. Q, K, V [T, H, d] bf16, d 64 or 128; log_decay [H]
     float32; S0 [N, H, d, d] float32, zero if not given. Returns O and the states
     after each sequence (``S`` may be S0: updated in place)."""
-    dev = _cuda_device(Q)
-    N = _starts("cu", cu, dev)
-    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
-    shape = (N, c.H, c.d, c.d)
-    _flat("S0", S0, shape, torch.float32, dev)
-    _flat("S", S, shape, torch.float32, dev)
-    with _On(dev, stream) as s:
-        ws, n = _workspace("vda_decay_attention_workspace", c, dev)
+    key = _signature(Q, K, V, log_decay, cu, S0, O, S)
+    key = key and ("decay", key, scale)
+    c, dev, n = _checked.get(key) or _remember(key, _check_decay(Q, K, V, log_decay, cu, S0, scale, O, S))
+
+    def make():
+        nonlocal O, S
+        ws = Q.new_empty(n, dtype=torch.uint8) if n else None
         if O is None:
-            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
         if S is None:
-            S = torch.empty(shape, dtype=torch.float32, device=dev)
-        st = lib().vda_decay_attention(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(log_decay), _ptr(cu),
-                                       _ptr(S0), _ptr(O), _ptr(S), _ptr(ws), n, s)
-    if st != VDA_OK:
-        raise VDAError(st, "vda_decay_attention")
+            S = Q.new_empty((c.N, c.H, c.d, c.d), dtype=torch.float32)
+        return (ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), log_decay.data_ptr(), cu.data_ptr(),
+                _addr(S0), O.data_ptr(), S.data_ptr(), _addr(ws), n)
+
+    _run("vda_decay_attention", dev, stream, make)
     return O, S
+
+
+def _check_decay_step(Q, K, V, log_decay, S, scale, O):
+    dev = _cuda_device(Q)
+    if S is None:
+        raise ValueError("S is required")
+    N = Q.shape[0]
+    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
+    _flat("S", S, (N, c.H, c.d, c.d), torch.float32, dev)
+    return c, dev
 
 
 def decay_attention_step(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay: torch.Tensor,
@@ -764,32 +824,24 @@ def decay_attention_step(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_
     """One token of every sequence through decay_attention's recurrence
     (vda_decay_attention_step): row n of Q, K, V [N, H, d] belongs to state S[n],
     which is updated in place. Returns O [N, H, d]."""
-    dev = _cuda_device(Q)
-    N = Q.shape[0]
-    c = _decay_config(Q, K, V, O, log_decay, N, scale, dev)
-    _flat("S", S, (N, c.H, c.d, c.d), torch.float32, dev)
-    if S is None:
-        raise ValueError("S is required")
-    with _On(dev, stream) as s:
+    key = _signature(Q, K, V, log_decay, S, O)
+    key = key and ("decay step", key, scale)
+    c, dev = _checked.get(key) or _remember(key, _check_decay_step(Q, K, V, log_decay, S, scale, O))
+
+    def make():
+        nonlocal O
         if O is None:
-            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
-        if N == 0:
-            return O
-        st = lib().vda_decay_attention_step(ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(log_decay), _ptr(S),
-                                            _ptr(O), s)
-    if st != VDA_OK:
-        raise VDAError(st, "vda_decay_attention_step")
+            O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        return (ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), log_decay.data_ptr(), S.data_ptr(),
+                O.data_ptr())
+
+    if c.N == 0:
+        return torch.empty_like(Q, memory_format=torch.contiguous_format) if O is None else O
+    _run("vda_decay_attention_step", dev, stream, make)
     return O
 
 
-def decay_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
-                             log_decay: torch.Tensor, cu: torch.Tensor, S0: Optional[torch.Tensor] = None,
-                             dS: Optional[torch.Tensor] = None, scale: float = 1.0,
-                             out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
-    """Gradients of decay_attention (vda_decay_attention_backward) for dL/dO and,
-    where given, dL/dS of the last states: dQ, dK, dV (bf16, contiguous) and dS0
-    (float32). Rows outside the sequences are not written: uninitialised in
-    tensors made here, as they were in ``out``."""
+def _check_decay_backward(Q, K, V, dO, log_decay, cu, S0, dS, scale, out):
     dev = _cuda_device(Q)
     N = _starts("cu", cu, dev)
     if dO is None:
@@ -798,19 +850,40 @@ def decay_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, 
     shape = (N, c.H, c.d, c.d)
     _flat("S0", S0, shape, torch.float32, dev)
     _flat("dS", dS, shape, torch.float32, dev)
-    with _On(dev, stream) as s:
-        ws, n = _workspace("vda_decay_attention_backward_workspace", c, dev)
+    if out is not None:
+        for k, t in zip(("dQ", "dK", "dV"), out):
+            if t is None:
+                raise ValueError(f"out must hold {k}")
+            _flat(k, t, tuple(Q.shape), torch.bfloat16, dev)
+        _flat("dS0", out[3], shape, torch.float32, dev)
+    return c, dev, _workspace_bytes("vda_decay_attention_backward_workspace", c)
+
+
+def decay_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
+                             log_decay: torch.Tensor, cu: torch.Tensor, S0: Optional[torch.Tensor] = None,
+                             dS: Optional[torch.Tensor] = None, scale: float = 1.0,
+                             out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of decay_attention (vda_decay_attention_backward) for dL/dO and,
+    where given, dL/dS of the last states: dQ, dK, dV (bf16, contiguous) and dS0
+    (float32; not computed where ``out`` lacks it). Rows outside the sequences are
+    not written: uninitialised in tensors made here, as they were in ``out``."""
+    given = None if out is None else (out.get("dQ"), out.get("dK"), out.get("dV"), out.get("dS0"))
+    key = _signature(Q, K, V, dO, log_decay, cu, S0, dS, *(given or ()))
+    key = key and ("decay backward", key, scale)
+    c, dev, n = _checked.get(key) or _remember(
+        key, _check_decay_backward(Q, K, V, dO, log_decay, cu, S0, dS, scale, given))
+
+    def make():
+        nonlocal out
+        ws = Q.new_empty(n, dtype=torch.uint8) if n else None
         if out is None:
-            out = {k: torch.empty(Q.shape, dtype=Q.dtype, device=dev) for k in ("dQ", "dK", "dV")}
-            out["dS0"] = torch.empty(shape, dtype=torch.float32, device=dev)
-        for k in ("dQ", "dK", "dV"):
-            _flat(k, out[k], tuple(Q.shape), torch.bfloat16, dev)
-        _flat("dS0", out.get("dS0"), shape, torch.float32, dev)
-        st = lib().vda_decay_attention_backward(
-            ctypes.byref(c), _ptr(Q), _ptr(K), _ptr(V), _ptr(dO), _ptr(log_decay), _ptr(cu), _ptr(S0), _ptr(dS),
-            _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]), _ptr(out.get("dS0")), _ptr(ws), n, s)
-    if st != VDA_OK:
-        raise VDAError(st, "vda_decay_attention_backward")
+            out = {k: torch.empty_like(Q, memory_format=torch.contiguous_format) for k in ("dQ", "dK", "dV")}
+            out["dS0"] = Q.new_empty((c.N, c.H, c.d, c.d), dtype=torch.float32)
+        return (ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), dO.data_ptr(), log_decay.data_ptr(),
+                cu.data_ptr(), _addr(S0), _addr(dS), out["dQ"].data_ptr(), out["dK"].data_ptr(),
+                out["dV"].data_ptr(), _addr(out.get("dS0")), _addr(ws), n)
+
+    _run("vda_decay_attention_backward", dev, stream, make)
     return out
 
 
