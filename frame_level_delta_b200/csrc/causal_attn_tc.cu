@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "seq.cuh"
@@ -47,6 +48,7 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kThreads = 384;  // TMA warp, MMA warp, two idle ones, two streams of four softmax warps
 constexpr int kMinSplitBlocks = 4;
+constexpr uint32_t kFma = 0x92;  // pairs of eight whose exponentials the FMA pipe takes
 
 template <int D>
 struct CaCfg {
@@ -108,13 +110,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* rfull = qfull + 1;
   uint64_t* rempty = rfull + C::kRing;
   uint64_t* sfull = rempty + C::kRing;  // [2] logits of stream s in TMEM
-  uint64_t* pfull = sfull + 2;          // [2] probabilities of stream s in TMEM
-  uint64_t* pvdone = pfull + 2;         // [2] O of stream s accumulated
+  uint64_t* pfull = sfull + 2;          // [2][2] halves of the probabilities of stream s in TMEM
+  uint64_t* pvdone = pfull + 4;         // [2] O of stream s accumulated
   uint64_t* drain = pvdone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
-  static_assert((1 + 2 * C::kRing + 7) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
+  static_assert((1 + 2 * C::kRing + 9) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int hk = blockIdx.x % a.Hkv;
@@ -165,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&pvdone[i], 1);
     }
     mbar_init(drain, 1);
@@ -251,13 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&sfull[s]);
         };
         auto issue_pv = [&](int s, int j, int slot) -> bool {
-          if (!seq::bar_wait(&pfull[s], j & 1, abort_flag, a.status, a.wait_ns)) return false;
-          tc_fence_after();
           const uint64_t dv = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8, dv + kk * 128, C::kIdescO,
-                       (j > 0 || kk > 0) ? 1u : 0u);
+          for (int half = 0; half < 2; ++half) {
+            if (!seq::bar_wait(&pfull[2 * s + half], j & 1, abort_flag, a.status, a.wait_ns)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+              mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8, dv + kk * 128,
+                         C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+          }
           mma_commit(&pvdone[s]);
           return true;
         };
@@ -331,6 +337,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k0 = blk * kTile;
       if (!warp_wait(&sfull[s], j & 1)) { ok = false; break; }
       tc_fence_after();
+      if (k0 + kTile > nk) {
+        // The keys end inside this block: zero the value rows behind them. The
+        // block's ring position follows from the loading order; its copy must
+        // have landed first.
+        const int t = 2 * j + s;
+        const int pos = kSplit ? t + min(t + 2, nb_all) : 2 * j + 1;
+        const int slot = pos % C::kRing;
+        if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { ok = false; break; }
+        if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
+        fence_proxy_async_smem();
+      }
       if (any_live) {
         float x[kTile];
 #pragma unroll
@@ -341,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[c4 * 32 + k] = __uint_as_float(v[k]);
         }
-        if (k0 + kTile > min_lim) {
+        const bool masked = k0 + kTile > min_lim;
+        if (masked) {
           const int n = lim - k0;
 #pragma unroll
           for (int k = 0; k < kTile; ++k)
@@ -387,35 +405,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 ls2[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) ls2[q] = make_float2(0.f, 0.f);
+        // Three of eight pairs on the FMA pipe: the exponentials of two streams
+        // would keep the special-function units as long as the products keep the
+        // tensor cores. Not in masked blocks (its smallest value is not 0).
+        auto weights = [&](auto plain) {
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t w[16];
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 y = __ffma2_rn(make_float2(x[c4 * 32 + 2 * k], x[c4 * 32 + 2 * k + 1]), sl2, nm2);
-            const float p0 = seq::ex2_approx(y.x), p1 = seq::ex2_approx(y.y);
-            ls2[k & 3] = __fadd2_rn(ls2[k & 3], make_float2(p0, p1));
-            w[k] = seq::pack_bf16(p0, p1);
+            for (int k = 0; k < 16; ++k) {
+              const float2 y = __ffma2_rn(make_float2(x[c4 * 32 + 2 * k], x[c4 * 32 + 2 * k + 1]), sl2, nm2);
+              const float2 p = plain.value && (kFma >> (k & 7) & 1)
+                                   ? seq::ex2_fma(y)
+                                   : make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
+              ls2[k & 3] = __fadd2_rn(ls2[k & 3], p);
+              w[k] = seq::pack_bf16(p.x, p.y);
+            }
+            tmem_st16(sa + c4 * 16, w);
+            if (c4 == 1) {
+              // The first half of the keys: their product may start.
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&pfull[2 * s]);
+            }
           }
-          tmem_st16(sa + c4 * 16, w);
-        }
+        };
+        if (masked)
+          weights(std::false_type{});
+        else
+          weights(std::true_type{});
         l_run += ((ls2[0].x + ls2[0].y) + (ls2[1].x + ls2[1].y)) + ((ls2[2].x + ls2[2].y) + (ls2[3].x + ls2[3].y));
         tmem_st_wait();
-      }
-      if (k0 + kTile > nk) {
-        // The keys end inside this block: zero the value rows behind them. The
-        // block's ring position follows from the loading order; its copy must
-        // have landed first.
-        const int t = 2 * j + s;
-        const int pos = kSplit ? t + min(t + 2, nb_all) : 2 * j + 1;
-        const int slot = pos % C::kRing;
-        if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { ok = false; break; }
-        if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
-        fence_proxy_async_smem();
+      } else if (lane == 0) {
+        mbar_arrive(&pfull[2 * s]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[s]);
+      if (lane == 0) mbar_arrive(&pfull[2 * s + 1]);
     }
     // ---------------- epilogue
     const bool have = my_nb > 0;
