@@ -20,9 +20,12 @@
 //
 // One CTA takes one (sequence, head, job, segment) and walks the segment's
 // chunks with X in registers. Per chunk: S1 = Q K^T; masked and weighted, P = bf16
-// in TMEM; O = Q X^T with X rounded to bf16 in shared memory, scaled by a^(i+1) in
-// TMEM, then O += P V (outputs are bf16, so each of the two operand roundings adds
-// what the output's own rounding is); W = V'^T K, where V' = a^(n-1-j) v_j enters
+// in TMEM; O = Q X^T + (P / f_i) V, one accumulator, times f_i = a^(i+1) on the way
+// out, with X rounded to bf16 in shared memory (outputs are bf16, so each of the
+// two operand roundings adds what the output's own rounding is). f_i is held at
+// 2^-100 from below, so that P / f_i stays in range: where a head forgets faster,
+// 2^-100 of X, nothing next to the token's own term, stands for less.
+// W = V'^T K, where V' = a^(n-1-j) v_j enters
 // as three bf16 parts (24 bits together), so that the state, which is fp32
 // outside, keeps fp32 accuracy. W starts from zero in every chunk and is added to
 // X in registers: the tensor cores' accumulation rounds toward zero, and over a
@@ -92,7 +95,7 @@ struct DaJob {
   int q, k, v;               // which map plays which part
   int reverse;
   int init_t;                // the initial state is read transposed
-  float s_in, s_state, s_up; // factors of P V, of X Q and of the update
+  float s_in, s_out, s_up;   // factors of P V (beside X Q), of the output and of the update
   const float* init;         // [N, H, d, d], nullable (zero)
   float* last;               // [N, H, d, d], nullable
   __nv_bfloat16* out;
@@ -175,8 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   uint64_t* sfull = rempty + 6;
   uint64_t* pfull = sfull + 1;
   uint64_t* qxdone = pfull + 1;
-  uint64_t* oscaled = qxdone + 1;
-  uint64_t* odone = oscaled + 1;
+  uint64_t* odone = qxdone + 1;
   uint64_t* oempty = odone + 1;
   uint64_t* vpfull = oempty + 1;  // [kMakers]
   uint64_t* vpempty = vpfull + kMakers;
@@ -239,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     mbar_init(sfull, 1);
     mbar_init(pfull, 8);
     mbar_init(qxdone, 1);
-    mbar_init(oscaled, 8);
     mbar_init(odone, 1);
     mbar_init(oempty, 8);
     for (int i = 0; i < kMakers; ++i) {
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             mma_commit(qxdone);
             mma_commit(&rempty[slot_of(c, 0)]);
             mma_commit(&rempty[slot_of(c, 0)]);
-            if (!(ok = wait1(pfull, c) && wait1(oscaled, c) && wait1(&rfull[slot_of(c, 2)], c >> 1))) break;
+            if (!(ok = wait1(pfull, c) && wait1(&rfull[slot_of(c, 2)], c >> 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int kk = 0; kk < kC / 16; ++kk)
@@ -488,6 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       for (int c = 0; c < nch && ok; ++c) {
         int tok, n;
         chunk(c, tok, n);
+        // log2 of 1 / f_i; f_i is a^(i+1) forward, a^(distance from the end) backward.
+        const float e_inv = fminf(-g2 * (float)(rev ? max(0, n - 1 - i) : i + 1), 100.f);
+        const float inv = exp2f(e_inv);
         if (!(ok = warp_wait(sfull, c))) break;
         tc_fence_after();
         // Weight a^|i - j| of the pairs a row sees: j <= i forward, i <= j < n
@@ -509,11 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float wx = shared_float(t + 2 * k), wy = shared_float(t + 2 * k + 1);
-                w[k] = seq::pack_bf16(wx != 0.f ? __uint_as_float(v[2 * k]) * wx : 0.f,
-                                      wy != 0.f ? __uint_as_float(v[2 * k + 1]) * wy : 0.f);
+                w[k] = seq::pack_bf16(wx != 0.f ? __uint_as_float(v[2 * k]) * (wx * inv) : 0.f,
+                                      wy != 0.f ? __uint_as_float(v[2 * k + 1]) * (wy * inv) : 0.f);
               }
             } else {
-              const float base = power(g2, rev ? j0 - i : i - j0 - 31);
+              const float base = exp2f(fmaf(g2, (float)(rev ? j0 - i : i - j0 - 31), e_inv));
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float2 x = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
@@ -540,32 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull);
-        // The state's part of the output: a^(i+1) forward, a^(distance from the
-        // end) backward.
-        const float f = job.s_state * power(g2, rev ? n - 1 - i : i + 1);
-        if (!(ok = warp_wait(qxdone, c))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int u = 0; u < D / 64; ++u) {
-          uint32_t y[32];
-          seq::tmem_ld32(oa + u * 32, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 x =
-                __fmul2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), make_float2(f, f));
-            y[k] = __float_as_uint(x.x);
-            y[k + 1] = __float_as_uint(x.y);
-          }
-          seq::tmem_st32(oa + u * 32, y);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(oscaled);
         if (!(ok = warp_wait(odone, c))) break;
         tc_fence_after();
         // O into registers first: the next chunk's QX may then take its columns.
+        const float f = job.s_out * exp2f(-e_inv);
         uint32_t op[D / 64][16];
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
@@ -574,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            op[u][k] = seq::pack_bf16(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+            op[u][k] = seq::pack_bf16(__uint_as_float(y[2 * k]) * f, __uint_as_float(y[2 * k + 1]) * f);
         }
         tc_fence_before();
         __syncwarp();
@@ -908,7 +890,7 @@ cudaError_t launch_decay_attention(const vda_decay_config& c, const void* Q, con
   a.cu = cu;
   a.log_decay = log_decay;
   a.status = status;
-  a.job[0] = DaJob{0, 1, 2, 0, 0, c.scale, c.scale, 1.f, S0, S_last, static_cast<__nv_bfloat16*>(O), c.o_row};
+  a.job[0] = DaJob{0, 1, 2, 0, 0, 1.f, c.scale, 1.f, S0, S_last, static_cast<__nv_bfloat16*>(O), c.o_row};
   const void* ptr[4] = {Q, K, V, nullptr};
   const long long row[4] = {c.q_row, c.k_row, c.v_row, 0};
   return c.d == 128 ? launch_d<128>(c, a, ptr, row, 3, ws, s) : launch_d<64>(c, a, ptr, row, 3, ws, s);
@@ -925,7 +907,7 @@ cudaError_t launch_decay_attention_backward(const vda_decay_config& c, const voi
   a.status = status;
   const long long g_row = (long long)c.H * c.d;  // gradients are packed without gaps
   // Maps: 0 Q, 1 K, 2 V, 3 dO.
-  a.job[0] = DaJob{3, 2, 1, 0, 1, c.scale, c.scale, 1.f, S0, nullptr, static_cast<__nv_bfloat16*>(dQ), g_row};
+  a.job[0] = DaJob{3, 2, 1, 0, 1, 1.f, c.scale, 1.f, S0, nullptr, static_cast<__nv_bfloat16*>(dQ), g_row};
   a.job[1] = DaJob{2, 3, 0, 1, 1, c.scale, 1.f, c.scale, dS, nullptr, static_cast<__nv_bfloat16*>(dK), g_row};
   a.job[2] = DaJob{1, 0, 3, 1, 0, c.scale, 1.f, c.scale, dS, dS0, static_cast<__nv_bfloat16*>(dV), g_row};
   const void* ptr[4] = {Q, K, V, dO};
