@@ -184,6 +184,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   CbBars<D> b(smem + C::kBarOff);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 0 && lane == 0) {
+    b.init();
+    prefetch_tmap(&mQ);
+    prefetch_tmap(&mK);
+    prefetch_tmap(&mV);
+    prefetch_tmap(&mG);
+  }
+  if (warp == 1) {
+    tmem_alloc(b.tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   const int hk = blockIdx.x % a.Hkv;
   int kb;
   const int sq = seq::find_item(
@@ -194,7 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return (n + kTile - 1) / kTile;
       },
       kb);
-  if (sq < 0) return;
+  if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);
+    return;
+  }
   int q_lo, q_hi, k_lo, nk;
   seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
   key_range(a, sq, k_lo, nk);
@@ -207,22 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_it = tiles - i0;
   const int rows = a.tpt * a.G;
 
-  if (warp == 0 && lane == 0) {
-    b.init();
-    prefetch_tmap(&mQ);
-    prefetch_tmap(&mK);
-    prefetch_tmap(&mV);
-    prefetch_tmap(&mG);
-  }
   // Rows that no tile has (128 is not a multiple of G) are summed over too: zero.
   for (int r = rows + (int)threadIdx.x; r < kTile; r += kThreads)
     for (int t = 0; t < C::kRing; ++t) seq::zero_row(sR + t * C::kTileBytes, C::kAtoms, r, kTile);
   fence_proxy_async_smem();
-  if (warp == 1) {
-    tmem_alloc(b.tmem_slot, C::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
@@ -418,25 +422,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col = part % 2 * (D / 2);
       const float f = is_k ? a.scale : 1.f;
       const long long at = ((long long)(k_lo + (live ? key : k0)) * a.Hkv + hk) * D + col;
-      uint4* dst = reinterpret_cast<uint4*>((is_k ? a.dK : a.dV) + at);
       const uint32_t ga = tmem + lane_off + (is_k ? kDK : kDV) + col;
+      uint32_t w[D / 4];
 #pragma unroll
       for (int c4 = 0; c4 < D / 64; ++c4) {
         uint32_t v[32];
         seq::tmem_ld32(ga + c4 * 32, v);
         tmem_ld_wait();
-        if (!live) continue;
 #pragma unroll
-        for (int q8 = 0; q8 < 4; ++q8) {
-          uint32_t op[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            op[k] = n_it > 0 ? seq::pack_bf16(__uint_as_float(v[q8 * 8 + 2 * k]) * f,
-                                              __uint_as_float(v[q8 * 8 + 2 * k + 1]) * f)
-                             : 0u;
-          dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
-        }
+        for (int k = 0; k < 16; ++k)
+          w[c4 * 16 + k] =
+              n_it > 0 ? seq::pack_bf16(__uint_as_float(v[2 * k]) * f, __uint_as_float(v[2 * k + 1]) * f) : 0u;
       }
+      // Through the CTA's own tiles, which every product has read.
+      seq::store_rows<D / 2>(smem + (part * 4 + quad) * (32 * D), w, live ? (is_k ? a.dK : a.dV) + at : nullptr);
     }
   }
 
@@ -467,28 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   CbBars<D> b(smem + C::kBarOff);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = blockIdx.x % a.Hkv;
-  int idx;
-  const int sq = seq::find_item(
-      blockIdx.x / a.Hkv, a.N, b.scratch,
-      [&](int i) {
-        int lo, hi;
-        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
-        return (hi - lo + a.tpt - 1) / a.tpt;
-      },
-      idx);
-  if (sq < 0) return;
-  int q_lo, q_hi, k_lo, nk;
-  seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
-  key_range(a, sq, k_lo, nk);
-  const int nq = q_hi - q_lo;
-  idx = (nq + a.tpt - 1) / a.tpt - 1 - idx;  // longest first
-  const int t0 = idx * a.tpt;
-  const int shift = nk - nq;
-  const int last = min(t0 + a.tpt, nq) - 1;
-  const int n_it = (min(nk, max(0, shift + last + 1)) + kTile - 1) / kTile;
-  const int rows = a.tpt * a.G;
-
   if (warp == 0 && lane == 0) {
     b.init();
     prefetch_tmap(&mQ);
@@ -501,7 +478,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const int hk = blockIdx.x % a.Hkv;
+  int idx;
+  const int sq = seq::find_item(
+      blockIdx.x / a.Hkv, a.N, b.scratch,
+      [&](int i) {
+        int lo, hi;
+        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
+        return (hi - lo + a.tpt - 1) / a.tpt;
+      },
+      idx);
+  if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);
+    return;
+  }
+  int q_lo, q_hi, k_lo, nk;
+  seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
+  key_range(a, sq, k_lo, nk);
+  const int nq = q_hi - q_lo;
+  idx = (nq + a.tpt - 1) / a.tpt - 1 - idx;  // longest first
+  const int t0 = idx * a.tpt;
+  const int shift = nk - nq;
+  const int last = min(t0 + a.tpt, nq) - 1;
+  const int n_it = (min(nk, max(0, shift + last + 1)) + kTile - 1) / kTile;
+  const int rows = a.tpt * a.G;
+
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   int issued = 0;
@@ -637,24 +639,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       constexpr int kCols = D / 4;
       const long long at = ((long long)(q_lo + (live ? tok : t0)) * (a.Hkv * a.G) + hk * a.G + r % a.G) * D;
-      uint4* dst = reinterpret_cast<uint4*>(a.dQ + at + part * kCols);
+      uint32_t w[kCols / 2];
 #pragma unroll
       for (int c = 0; c < kCols / 16; ++c) {
         uint32_t v[16];
         tmem_ld16(tmem + lane_off + kDQ + part * kCols + c * 16, v);
         tmem_ld_wait();
-        if (!live) continue;
 #pragma unroll
-        for (int q8 = 0; q8 < 2; ++q8) {
-          uint32_t op[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            op[k] = n_it > 0 ? seq::pack_bf16(__uint_as_float(v[q8 * 8 + 2 * k]) * a.scale,
-                                              __uint_as_float(v[q8 * 8 + 2 * k + 1]) * a.scale)
-                             : 0u;
-          dst[c * 2 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
-        }
+        for (int k = 0; k < 8; ++k)
+          w[c * 8 + k] = n_it > 0 ? seq::pack_bf16(__uint_as_float(v[2 * k]) * a.scale,
+                                                   __uint_as_float(v[2 * k + 1]) * a.scale)
+                                  : 0u;
       }
+      seq::store_rows<kCols>(smem + (part * 4 + quad) * (32 * kCols * 2), w, live ? a.dQ + at + part * kCols : nullptr);
     }
   }
 

@@ -119,46 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert((1 + 2 * C::kRing + 9) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = blockIdx.x % a.Hkv;
-  const int rest = blockIdx.x / a.Hkv;
-  const int z = kSplit ? rest % a.nsplit : 0;
-  const int per_item = kSplit ? a.tpt : 2 * a.tpt;
-  int idx;
-  const int sq = seq::find_item(
-      kSplit ? rest / a.nsplit : rest, a.N, scratch,
-      [&](int i) {
-        int lo, hi;
-        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
-        return (hi - lo + per_item - 1) / per_item;
-      },
-      idx);
-  if (sq < 0) return;
-  int q_lo, q_hi, k_lo, nk;
-  seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
-  key_range(a, sq, k_lo, nk);
-  const int nq = q_hi - q_lo;
-  // Longest tiles first: a sequence's last rows see the most keys.
-  idx = (nq + per_item - 1) / per_item - 1 - idx;
-  // Per stream: first token within the sequence and key blocks seen.
-  int t0[2], nb[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    t0[s] = idx * per_item + (kSplit ? 0 : s * a.tpt);
-    const int last = min(t0[s] + a.tpt, nq) - 1;
-    const int seen = t0[s] < nq ? min(nk, max(0, nk - nq + last + 1)) : 0;
-    nb[s] = (seen + kTile - 1) / kTile;
-  }
-  int b_lo = 0;  // first key block of this CTA's share
-  if (kSplit) {
-    const int used = used_splits(nb[0], a.nsplit);
-    if (z >= used) return;
-    b_lo = (int)((long long)nb[0] * z / used);
-    const int n = (int)((long long)nb[0] * (z + 1) / used) - b_lo;
-    nb[0] = (n + 1) / 2;
-    nb[1] = n / 2;
-  }
-  const int nb_all = kSplit ? nb[0] + nb[1] : max(nb[0], nb[1]);
-
   if (warp == 0 && lane == 0) {
     mbar_init(qfull, 1);
     for (int i = 0; i < C::kRing; ++i) {
@@ -183,7 +143,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const int hk = blockIdx.x % a.Hkv;
+  const int rest = blockIdx.x / a.Hkv;
+  const int z = kSplit ? rest % a.nsplit : 0;
+  const int per_item = kSplit ? a.tpt : 2 * a.tpt;
+  int idx;
+  const int sq = seq::find_item(
+      kSplit ? rest / a.nsplit : rest, a.N, scratch,
+      [&](int i) {
+        int lo, hi;
+        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
+        return (hi - lo + per_item - 1) / per_item;
+      },
+      idx);
+  // (The list's search synchronises the block behind the set-up above.)
+  auto leave = [&] {
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(*tmem_slot, C::kTmemCols);
+  };
+  if (sq < 0) {
+    leave();
+    return;
+  }
+  int q_lo, q_hi, k_lo, nk;
+  seq::bounds(a.cu_q, sq, a.Tq, q_lo, q_hi);
+  key_range(a, sq, k_lo, nk);
+  const int nq = q_hi - q_lo;
+  // Longest tiles first: a sequence's last rows see the most keys.
+  idx = (nq + per_item - 1) / per_item - 1 - idx;
+  // Per stream: first token within the sequence and key blocks seen.
+  int t0[2], nb[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    t0[s] = idx * per_item + (kSplit ? 0 : s * a.tpt);
+    const int last = min(t0[s] + a.tpt, nq) - 1;
+    const int seen = t0[s] < nq ? min(nk, max(0, nk - nq + last + 1)) : 0;
+    nb[s] = (seen + kTile - 1) / kTile;
+  }
+  int b_lo = 0;  // first key block of this CTA's share
+  if (kSplit) {
+    const int used = used_splits(nb[0], a.nsplit);
+    if (z >= used) {
+      leave();
+      return;
+    }
+    b_lo = (int)((long long)nb[0] * z / used);
+    const int n = (int)((long long)nb[0] * (z + 1) / used) - b_lo;
+    nb[0] = (n + 1) / 2;
+    nb[1] = n / 2;
+  }
+  const int nb_all = kSplit ? nb[0] + nb[1] : max(nb[0], nb[1]);
+
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -473,24 +483,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         if (live && a.lse) a.lse[row] = seen ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
-        uint4* dst = reinterpret_cast<uint4*>(a.O + tok_g * a.o_row + (long long)head * D);
+        uint32_t w[D / 2];
 #pragma unroll
         for (int c4 = 0; c4 < D / 32; ++c4) {
           uint32_t v[32];
           seq::tmem_ld32(oa + c4 * 32, v);
           tmem_ld_wait();
-          if (!live) continue;
 #pragma unroll
-          for (int q8 = 0; q8 < 4; ++q8) {
-            uint32_t op[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              op[k] = seen ? seq::pack_bf16(__uint_as_float(v[q8 * 8 + 2 * k]) * inv,
-                                            __uint_as_float(v[q8 * 8 + 2 * k + 1]) * inv)
-                           : 0u;
-            dst[c4 * 4 + q8] = make_uint4(op[0], op[1], op[2], op[3]);
-          }
+          for (int k = 0; k < 16; ++k)
+            w[c4 * 16 + k] =
+                seen ? seq::pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv) : 0u;
         }
+        // Through the stream's own Q tile, which its products have read. (Where it has
+        // none, the tile's copy must have landed.)
+        if (!have && nb_all > 0) warp_wait(qfull, 0);
+        seq::store_rows<D>(sQ + s * C::kTileBytes + quad * (32 * D * 2), w,
+                           live ? a.O + tok_g * a.o_row + (long long)head * D : nullptr);
       }
     }
   }

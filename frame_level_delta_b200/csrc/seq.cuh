@@ -178,6 +178,33 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], const void* p)
                : "memory");
 }
 
+// Stores a warp's 32 rows of kCols bf16 values, one row per lane (w: the lane's
+// packed row; row: where it goes, null for a row that is none), through 32 x kCols
+// values of shared memory that only this warp uses: the lanes of a store then write
+// whole rows. (Row by row from the lanes that hold them, a store touches 32 lines;
+// a tile's epilogue took 4500 cycles.)
+template <int kCols>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[kCols / 2], __nv_bfloat16* row) {
+  constexpr int kChunks = kCols / 8, kPer = 32 / kChunks;  // 16-byte chunks per row; rows per store
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int r, int c) {
+    // The 8 lanes of a phase hit 8 different 16-byte columns.
+    const int x = kChunks >= 8 ? r & 7 : (r * kChunks / 8) & (kChunks - 1);
+    return reinterpret_cast<uint4*>(stage + r * (kCols * 2) + ((c ^ x) * 16));
+  };
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) *at(lane, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  const int c = lane % kChunks;
+#pragma unroll
+  for (int it = 0; it < kChunks; ++it) {
+    const int r = it * kPer + lane / kChunks;
+    const unsigned long long p = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r);
+    const uint4 v = *at(r, c);
+    if (p) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + c * 8) = v;
+  }
+}
+
 // 3-D tiled bulk tensor copy shared -> global (the issuing thread's bulk group),
 // and the wait until the group's copies have read shared memory.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
