@@ -105,6 +105,7 @@ struct DaJob {
 struct DaArgs {
   int N, H, T, njobs;
   int seg;                  // chunks per segment
+  int items;                // entries of seg_state: segments of all sequences, at most
   const int* cu;
   const float* log_decay;   // [H]
   DaJob job[kMaxJobs];
@@ -718,6 +719,8 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   }
   if (before) atomicAdd(&first_s, before);
   __syncthreads();
+  // Sequences that overlap (a wrong prefix array) have more segments than there is room for.
+  if (first_s + nparts > a.items) return;
   const int e = (slice * 256 + threadIdx.x) * 4;
   const int r = e / D, c = e % D;
   const float g2 = head_decay(a, h);
@@ -842,6 +845,7 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
   a.seg = segment_chunks(c, a.njobs);
   const bool whole = (long long)c.T <= (long long)a.seg * kC;  // no sequence can be longer than a segment
   const long long items = segment_items(c, a.seg);
+  a.items = (int)items;
   a.seg_state = whole ? nullptr : static_cast<float*>(ws);
   a.wait_ns = 2000000000u;
   const long long grid = items * c.H * a.njobs;
