@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* sX = smem + C::kXOff;
-  uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [2][3] chunk parity; Q, K, V
+  uint64_t* rfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [6], see slot_of
   uint64_t* rempty = rfull + 6;
   uint64_t* sfull = rempty + 6;
   uint64_t* pfull = sfull + 1;
@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   };
   // A slot is free after two arrivals: of Q, two commits behind QX; of K, QK's and
   // W's; of V, W's (V' has been read) and the output tile's.
-  auto slot_of = [&](int c, int t) { return (c & 1) * 3 + t; };
+  // The six slots hold two chunks' tiles, or, without Q, three chunks'.
+  constexpr int kStages = kStateOnly ? 3 : 2;
+  auto slot_of = [&](int c, int t) { return kStateOnly ? c % 3 * 2 + t - 1 : (c & 1) * 3 + t; };
   auto tile_of = [&](int c, int t) { return smem + slot_of(c, t) * C::kTileBytes; };
 
   if (warp == 0 && lane == 0) {
@@ -305,11 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     const int c = g / C::kSteps, q = g % C::kSteps;
     int tok, n;
     chunk(c, tok, n);
-    if (!warp_wait(&rfull[slot_of(c, 2)], c >> 1)) return false;
+    if (!warp_wait(&rfull[slot_of(c, 2)], c / kStages)) return false;
     if (n < kC && q < kMakers) {
       // Key and value rows behind the sequence are zeroed (by every group: each
       // reads and signals steps of its own).
-      if (!warp_wait(&rfull[slot_of(c, 1)], c >> 1)) return false;
+      if (!warp_wait(&rfull[slot_of(c, 1)], c / kStages)) return false;
       if (row >= n) {
         seq::zero_row(tile_of(c, 1), C::kAtoms, row, kC);
         seq::zero_row(tile_of(c, 2), C::kAtoms, row, kC);
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
           for (int t = kStateOnly ? 1 : 0; t < 3; ++t) {
             const CUtensorMap* m = &maps.m[t == 0 ? job.q : t == 1 ? job.k : job.v];
             uint64_t* full = &rfull[slot_of(c, t)];
-            if (!(ok = wait1(&rempty[slot_of(c, t)], (c >> 1) + 1))) break;
+            if (!(ok = wait1(&rempty[slot_of(c, t)], c / kStages + 1))) break;
             mbar_arrive_expect_tx(full, C::kTileBytes);
 #pragma unroll
             for (int at = 0; at < C::kAtoms; ++at)
@@ -377,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         }
         if (*abort_flag) {
           // Let every issued copy land before the CTA's shared memory is released.
-          for (int i = max(0, loaded - 6); i < loaded; ++i)
+          for (int i = max(0, loaded - 3 * kStages); i < loaded; ++i)
             if (!kStateOnly || i % 3 != 0)
-              mbar_wait(&rfull[slot_of(i / 3, i % 3)], (i / 6) & 1, nullptr, a.status, a.wait_ns);
+              mbar_wait(&rfull[slot_of(i / 3, i % 3)], (i / 3 / kStages) & 1, nullptr, a.status, a.wait_ns);
         }
       }
     } else if (warp == 1) {
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             const uint64_t dv = smem_desc_sw128(smem_u32(tile_of(c, 2)), kC * 128, 1024);
             const uint64_t dx = smem_desc_sw128(opaque(smem_u32(sX)), 16, 1024);
             const uint32_t tm = opaque(tmem);
-            if (!(ok = wait1(&rfull[slot_of(c, 0)], c >> 1) && wait1(&rfull[slot_of(c, 1)], c >> 1))) break;
+            if (!(ok = wait1(&rfull[slot_of(c, 0)], c / kStages) && wait1(&rfull[slot_of(c, 1)], c / kStages))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
             mma_commit(qxdone);
             mma_commit(&rempty[slot_of(c, 0)]);
             mma_commit(&rempty[slot_of(c, 0)]);
-            if (!(ok = wait1(pfull, c) && wait1(&rfull[slot_of(c, 2)], c >> 1))) break;
+            if (!(ok = wait1(pfull, c) && wait1(&rfull[slot_of(c, 2)], c / kStages))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int kk = 0; kk < kC / 16; ++kk)
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
           const uint64_t dk = smem_desc_sw128(smem_u32(tile_of(c, 1)), kC * 128, 1024);
-          if (!(ok = wait1(&rfull[slot_of(c, 1)], c >> 1))) break;
+          if (!(ok = wait1(&rfull[slot_of(c, 1)], c / kStages))) break;
 #pragma unroll 1
           for (int q = 0; q < C::kSteps; ++q) {
             const int g = c * C::kSteps + q, maker = g % kMakers;
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         uint8_t* vt = tile_of(c, 2);
         if (n < kC) {
           // Value rows behind the sequence are zeroed: 0 x NaN is NaN.
-          if (!(ok = warp_wait(&rfull[slot_of(c, 2)], c >> 1))) break;
+          if (!(ok = warp_wait(&rfull[slot_of(c, 2)], c / kStages))) break;
           if (i >= n) seq::zero_row(vt, C::kAtoms, i, kC);
           fence_proxy_async_smem();
         }
