@@ -199,13 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hk = blockIdx.x % a.Hkv;
   int kb;
   const int sq = seq::find_item(
-      blockIdx.x / a.Hkv, a.N, b.scratch,
+      blockIdx.x / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
       [&](int i) {
         int lo, n;
         key_range(a, i, lo, n);
-        return (n + kTile - 1) / kTile;
+        return n;
       },
-      kb);
+      [&](int n) { return (n + kTile - 1) / kTile; }, kb);
   if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);
@@ -481,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hk = blockIdx.x % a.Hkv;
   int idx;
   const int sq = seq::find_item(
-      blockIdx.x / a.Hkv, a.N, b.scratch,
+      blockIdx.x / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
       [&](int i) {
         int lo, hi;
         seq::bounds(a.cu_q, i, a.Tq, lo, hi);
-        return (hi - lo + a.tpt - 1) / a.tpt;
+        return hi - lo;
       },
-      idx);
+      [&](int n) { return (n + a.tpt - 1) / a.tpt; }, idx);
   if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);

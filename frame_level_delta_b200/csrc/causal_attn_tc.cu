@@ -149,13 +149,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per_item = kSplit ? a.tpt : 2 * a.tpt;
   int idx;
   const int sq = seq::find_item(
-      kSplit ? rest / a.nsplit : rest, a.N, scratch,
+      kSplit ? rest / a.nsplit : rest, a.N, scratch, reinterpret_cast<int*>(sQ),
       [&](int i) {
         int lo, hi;
         seq::bounds(a.cu_q, i, a.Tq, lo, hi);
-        return (hi - lo + per_item - 1) / per_item;
+        return hi - lo;
       },
-      idx);
+      [&](int n) { return (n + per_item - 1) / per_item; }, idx);
   // (The list's search synchronises the block behind the set-up above.)
   auto leave = [&] {
     tc_fence_after();

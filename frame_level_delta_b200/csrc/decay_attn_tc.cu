@@ -131,6 +131,23 @@ __device__ __forceinline__ void chunk_tokens(int len, int reverse, int p0, int p
   hi = min(len, reverse ? (nch - p0) * kC : p1 * kC);
 }
 
+// Segments of the sequences before sequence sq: where its own begin in seg_state.
+// Every thread of the block calls it.
+__device__ __forceinline__ int segments_before(const DaArgs& a, int sq, int* scratch) {
+  const int seg_tokens = a.seg * kC;
+  if (threadIdx.x == 0) *scratch = 0;
+  __syncthreads();
+  int n = 0;
+  for (int i = threadIdx.x; i < sq; i += blockDim.x) {
+    int lo, hi;
+    seq::bounds(a.cu, i, a.T, lo, hi);
+    n += max(1, (hi - lo + seg_tokens - 1) / seg_tokens);
+  }
+  if (n) atomicAdd(scratch, n);
+  __syncthreads();
+  return *scratch;
+}
+
 // x = hi + mid + lo, each a bf16 (the upper half of a word), exactly: 8 bits of
 // the 24 each, cut off, not rounded. Returns the packed pairs of two values.
 __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
@@ -203,26 +220,31 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   const DaJob& job = a.job[jb];
   const int seg_tokens = a.seg * kC;
   int part;
+  // An empty sequence still has a state. The launch that forms states leaves out a
+  // sequence's last segment: nothing follows it.
   const int sq = seq::find_item(
-      item, a.N, scratch,
+      item, a.N, scratch, reinterpret_cast<int*>(smem),
       [&](int i) {
         int lo, hi;
         seq::bounds(a.cu, i, a.T, lo, hi);
-        return max(1, (hi - lo + seg_tokens - 1) / seg_tokens);  // an empty sequence still has a state
+        return hi - lo;
       },
-      part);
+      [&](int n) { return max(1, (n + seg_tokens - 1) / seg_tokens) - (kStateOnly ? 1 : 0); }, part);
   if (sq < 0) return;
   int lo, hi;
   seq::bounds(a.cu, sq, a.T, lo, hi);
   const int len = hi - lo;
   const int nch_all = (len + kC - 1) / kC;
   const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
-  if (kStateOnly && part == nparts - 1) return;  // nothing follows the last segment
   const int p0 = part * a.seg, nch = min(nch_all, p0 + a.seg) - p0;
   const int rev = job.reverse;
   const float g2 = head_decay(a, h);
   const long long st_off = ((long long)sq * a.H + h) * (D * D);
-  float* seg_state = a.seg_state ? a.seg_state + (((long long)item * a.H + h) * a.njobs + jb) * (D * D) : nullptr;
+  float* seg_state = nullptr;
+  if (a.seg_state && nparts > 1) {
+    const int at = segments_before(a, sq, scratch) + part;
+    if (at < a.items) seg_state = a.seg_state + (((long long)at * a.H + h) * a.njobs + jb) * (D * D);
+  }
   // First token (within the tensor) and token count of processing-order chunk c.
   auto chunk = [&](int c, int& tok, int& n) {
     const int cc = rev ? nch_all - 1 - (p0 + c) : p0 + c;
@@ -700,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
 template <int D>
 __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DaArgs a) {
   constexpr int kBatch = 8;
-  __shared__ int first_s;
+  __shared__ int scratch;
   const int sq = blockIdx.y;
   const int jb = blockIdx.x % a.njobs, h = (blockIdx.x / a.njobs) % a.H;
   const int slice = blockIdx.x / a.njobs / a.H;
@@ -711,16 +733,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   const int len = hi - lo;
   const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
   if (nparts == 1) return;
-  if (threadIdx.x == 0) first_s = 0;
-  __syncthreads();
-  int before = 0;  // items of the sequences before this one
-  for (int i = threadIdx.x; i < sq; i += blockDim.x) {
-    int x, y;
-    seq::bounds(a.cu, i, a.T, x, y);
-    before += max(1, (y - x + seg_tokens - 1) / seg_tokens);
-  }
-  if (before) atomicAdd(&first_s, before);
-  __syncthreads();
+  const int first_s = segments_before(a, sq, &scratch);
   // Sequences that overlap (a wrong prefix array) have more segments than there is room for.
   if (first_s + nparts > a.items) return;
   const int e = (slice * 256 + threadIdx.x) * 4;
@@ -869,7 +882,9 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
   if ((e = set_max_dynamic_smem(main_fn, C::kSmemBytes)) != cudaSuccess) return e;
   if ((e = set_max_dynamic_smem(state_fn, C::kSmemBytes)) != cudaSuccess) return e;
   if (!whole) {
-    decay_attn_tc_kernel<D, true><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(maps, a);
+    // Segments that another one follows: at most T / (a segment's tokens) of them.
+    const long long states = (long long)c.T / ((long long)a.seg * kC) * c.H * a.njobs;
+    decay_attn_tc_kernel<D, true><<<(unsigned)states, kThreads, C::kSmemBytes, s>>>(maps, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const dim3 jg((unsigned)(c.H * a.njobs * (D * D / 1024)), (unsigned)c.N);
     decay_join_kernel<D><<<jg, 256, 0, s>>>(a);

@@ -19,17 +19,33 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int T, int& lo, int
   hi = min(max(__ldg(cu + i + 1), lo), T);
 }
 
-// Work item x of a list in which sequence i has count(i) items: returns the
-// sequence and x's index within it, or -1 past the list's end. Every thread of
-// the block calls it; `scratch` holds 40 ints. Each pass takes blockDim.x
+// Work item x of a list in which a sequence of size n has count(n) items (size(i):
+// sequence i's tokens): returns the sequence and x's index within it, or -1 past the
+// list's end. Up to kSorted sequences, the largest come first, so that no long one
+// starts when the others are done; beyond, in their order. Every thread of the block
+// calls it; `scratch` holds 40 ints, `big` 2 kSorted. Each pass takes blockDim.x
 // sequences (one load and one scan), so up to that many cost one pass.
-template <typename Count>
-__device__ __forceinline__ int find_item(int x, int N, int* scratch, Count count, int& idx) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (threadIdx.x == 0) scratch[33] = -1;
+constexpr int kSorted = 128;
+template <typename Size, typename Count>
+__device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, Size size, Count count, int& idx) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
+  if (t == 0) scratch[33] = -1;
+  const bool sorted = N > 1 && N <= kSorted;
+  int own = 0;
+  if (sorted) {
+    if (t < N) big[t] = own = size(t);
+    __syncthreads();
+    if (t < N) {
+      int rank = 0;
+      for (int j = 0; j < N; ++j) rank += big[j] > own || (big[j] == own && j < t);
+      big[kSorted + rank] = t;
+    }
+    __syncthreads();
+  }
   for (int base = 0; base < N; base += blockDim.x) {
-    const int i = base + threadIdx.x;
-    const int c = i < N ? count(i) : 0;
+    const int i = base + t;
+    const int sq = sorted && i < N ? big[kSorted + i] : i;
+    const int c = i < N ? count(sorted ? big[sq] : size(sq)) : 0;
     int inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -40,19 +56,20 @@ __device__ __forceinline__ int find_item(int x, int N, int* scratch, Count count
     __syncthreads();
     int off = 0, total = 0;
     for (int w = 0; w < warps; ++w) {
-      const int t = scratch[w];
-      if (w < warp) off += t;
-      total += t;
+      const int n = scratch[w];
+      if (w < warp) off += n;
+      total += n;
     }
     const int hi = off + inc, lo = hi - c;
     if (x >= lo && x < hi) {
-      scratch[33] = i;
+      scratch[33] = sq;
       scratch[34] = x - lo;
     }
     __syncthreads();
     if (scratch[33] >= 0) break;
     x -= total;
   }
+  sm100::fence_proxy_async_smem();  // copies may land in `big` from here on
   __syncthreads();
   idx = scratch[34];
   return scratch[33];
