@@ -11,15 +11,18 @@
 // independent in every product, so rows that do not exist (G not dividing 128,
 // tokens past the sequence) carry what lies there and are not stored.
 //
-// One CTA runs two streams of softmax rows, each with its own four warps, its own
-// logits S and its own accumulator O in TMEM (S 2 x 128 columns, O 2 x D; the
-// probabilities overwrite their logits as packed bf16), so that the tensor cores
-// work on one stream's products while the other's exponentials run:
-//  - prompts: the streams are two consecutive tiles and share each key block;
-//  - few rows on long keys (single new tokens): both streams are the same tile,
-//    stream s takes key blocks s, s + 2, ... of this CTA's share of the keys, and
-//    each leaves a partial (o normalised by its own l, its log-sum) that a second
-//    kernel joins.
+// Prompts: a CTA runs two streams, two consecutive tiles that share each key block,
+// each with its own four softmax warps, its own logits S and its own accumulator O in
+// TMEM (S 2 x 128 columns, O 2 x D; the probabilities overwrite their logits as
+// packed bf16), so that the tensor cores work on one stream's products while the
+// other's exponentials run.
+//
+// Few rows on long keys (single new tokens) are bound by the bytes of K and V, and
+// by how evenly sequences of different lengths fill the SMs: a CTA has one stream and
+// half the shared memory and TMEM, two run on an SM, so that one's start and end hide
+// behind the other's copies, and a tile's key blocks are shared out over several
+// CTAs, each of which leaves a partial (o normalised by its own l, its log-sum) that
+// a second kernel joins.
 //
 // Per key block: S = Q K^T (M = 128, N = 128), m = running row maximum in the
 // log2 domain, P = 2^(S s log2(e) - m) rounded to bf16 (the tensor cores' operand
@@ -46,24 +49,28 @@ namespace vda {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 384;  // TMA warp, MMA warp, two idle ones, two streams of four softmax warps
 constexpr int kMinSplitBlocks = 4;
+constexpr int kSplitCtas = 8;  // CTAs per SM that the split form aims at
 constexpr uint32_t kFma = 0x92;  // pairs of eight whose exponentials the FMA pipe takes
 
-template <int D>
+template <int D, int kStreams>
 struct CaCfg {
+  static constexpr int kThreads = 128 + 128 * kStreams;  // TMA warp, MMA warp, two idle ones, four warps a stream
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kRing = D == 128 ? 5 : 10;  // key and value blocks in flight, one ring
+  // Key and value blocks in flight, one ring.
+  static constexpr int kRing = kStreams == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
   static constexpr int kQOff = 0;
-  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kRingOff = kStreams * kTileBytes;
   static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;
-  static constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 256 + D;
-  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kS = 0, kO = 128 * kStreams;  // stream s: + 128 s, + D s columns
+  static constexpr uint32_t kTmemCols = kStreams == 2 ? 512 : 256;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescO = sm100::idesc_bf16_f32(128, D, false, true);
-  static_assert(kSmemBytes <= 232448, "more shared memory than a CTA may use");
+  // 227 KB to a CTA; 228 KB to an SM, 1 KB of it taken by each CTA.
+  static_assert(kSmemBytes <= (kStreams == 2 ? 232448 : 115712), "more shared memory than a CTA may use");
+  static_assert(kRingOff >= 8 * seq::kSorted, "the list's search works in the Q tiles");
 };
 
 struct CaArgs {
@@ -75,8 +82,8 @@ struct CaArgs {
   __nv_bfloat16* O;
   long long o_row;
   float* lse;          // [Tq, Hq], nullable
-  float* part_o;       // split form: [2 nsplit][Tq * Hq][D]
-  float* part_l;       // split form: [2 nsplit][Tq * Hq], log2 domain
+  float* part_o;       // split form: [nsplit][Tq * Hq][D]
+  float* part_l;       // split form: [nsplit][Tq * Hq], log2 domain
   uint32_t* status;
   uint32_t wait_ns;
 };
@@ -97,10 +104,11 @@ __device__ __forceinline__ int used_splits(int nb, int nsplit) {
 }
 
 template <int D, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((CaCfg<D, kSplit ? 1 : 2>::kThreads), (kSplit ? 2 : 1))
     causal_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                           const __grid_constant__ CUtensorMap mV, const CaArgs a) {
-  using C = CaCfg<D>;
+  constexpr int kStreams = kSplit ? 1 : 2;
+  using C = CaCfg<D, kStreams>;
   using namespace sm100;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hk = blockIdx.x % a.Hkv;
   const int rest = blockIdx.x / a.Hkv;
   const int z = kSplit ? rest % a.nsplit : 0;
-  const int per_item = kSplit ? a.tpt : 2 * a.tpt;
+  const int per_item = kStreams * a.tpt;
   int idx;
   const int sq = seq::find_item(
       kSplit ? rest / a.nsplit : rest, a.N, scratch, reinterpret_cast<int*>(sQ),
@@ -172,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Longest tiles first: a sequence's last rows see the most keys.
   idx = (nq + per_item - 1) / per_item - 1 - idx;
   // Per stream: first token within the sequence and key blocks seen.
-  int t0[2], nb[2];
+  int t0[2], nb[2] = {0, 0};
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    t0[s] = idx * per_item + (kSplit ? 0 : s * a.tpt);
+  for (int s = 0; s < kStreams; ++s) {
+    t0[s] = idx * per_item + s * a.tpt;
     const int last = min(t0[s] + a.tpt, nq) - 1;
     const int seen = t0[s] < nq ? min(nk, max(0, nk - nq + last + 1)) : 0;
     nb[s] = (seen + kTile - 1) / kTile;
@@ -188,26 +196,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     b_lo = (int)((long long)nb[0] * z / used);
-    const int n = (int)((long long)nb[0] * (z + 1) / used) - b_lo;
-    nb[0] = (n + 1) / 2;
-    nb[1] = n / 2;
+    nb[0] = (int)((long long)nb[0] * (z + 1) / used) - b_lo;
   }
-  const int nb_all = kSplit ? nb[0] + nb[1] : max(nb[0], nb[1]);
+  const int nb_all = max(nb[0], nb[1]);
 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // 384 threads start with 168 registers each; the first four warps give most of
-  // theirs to the rows' 128 logits (56 + 2 x 224 = 504 = 3 x 168).
+  // 384 (256) threads start with 168 (128) registers each; the first four warps give
+  // most of theirs to the rows' 128 logits (56 + 2 x 224 = 504 = 3 x 168; 48 + 208 =
+  // 256 = 2 x 128).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kSplit)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---------------- TMA producer. Ring order is the order in which the MMA
-      // warp takes blocks: K0 (K1 in the split form, one per stream), then V_t and
-      // the next K in turn.
+      // warp takes blocks: K0, then V_t and the next K in turn.
       if (nb_all > 0 && seq::elect_one()) {
         const uint32_t q_bytes = (uint32_t)(a.tpt * a.G) * 128u;
-        const int tiles = (!kSplit && nb[1] > 0) ? 2 : 1;
+        const int tiles = nb[1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * tiles);
         for (int s = 0; s < tiles; ++s)
 #pragma unroll
@@ -225,12 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
           return true;
         };
-        constexpr int ahead = kSplit ? 2 : 1;
         bool ok = load(&mK, 0);
-        if (kSplit && ok && nb_all > 1) ok = load(&mK, 1);
         for (int t = 0; t < nb_all && ok; ++t) {
           ok = load(&mV, t);
-          if (ok && t + ahead < nb_all) ok = load(&mK, t + ahead);
+          if (ok && t + 1 < nb_all) ok = load(&mK, t + 1);
         }
         if (*abort_flag) {
           // Let every issued copy land before the CTA's shared memory is released.
@@ -254,12 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto issue_s = [&](int s, int slot) {
           // The address field of a descriptor counts 16 bytes: steps are added to it.
-          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + (kSplit ? 0 : s) * C::kTileBytes), 16, 1024);
+          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + s * C::kTileBytes), 16, 1024);
           const uint64_t dk = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) / 16;
-            mma_f16(tmem + (s ? C::kS1 : C::kS0), dq + off, dk + off, C::kIdescS, kk > 0 ? 1u : 0u);
+            mma_f16(tmem + C::kS + s * 128, dq + off, dk + off, C::kIdescS, kk > 0 ? 1u : 0u);
           }
           mma_commit(&sfull[s]);
         };
@@ -271,49 +278,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-              mma_f16_ts(tmem + (s ? C::kO1 : C::kO0), tmem + (s ? C::kS1 : C::kS0) + kk * 8, dv + kk * 128,
-                         C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+              mma_f16_ts(tmem + C::kO + s * D, tmem + C::kS + s * 128 + kk * 8, dv + kk * 128, C::kIdescO,
+                         (j > 0 || kk > 0) ? 1u : 0u);
           }
           mma_commit(&pvdone[s]);
           return true;
         };
         int slot = 0, vslot = 0;
         if (ok && nb_all > 0) {
-          if (kSplit) {
-            for (int s = 0; s < min(2, nb_all) && ok; ++s) {
-              if (!(ok = take(slot))) break;
-              issue_s(s, slot);
-              mma_commit(&rempty[slot]);
-            }
-            for (int t = 0; t < nb_all && ok; ++t) {
-              if (!(ok = take(vslot)) || !(ok = issue_pv(t & 1, t >> 1, vslot))) break;
-              mma_commit(&rempty[vslot]);
-              if (t + 2 < nb_all) {
-                if (!(ok = take(slot))) break;
-                issue_s(t & 1, slot);
-                mma_commit(&rempty[slot]);
+          if ((ok = take(slot))) {
+            for (int s = 0; s < kStreams; ++s)
+              if (nb[s] > 0) issue_s(s, slot);
+            mma_commit(&rempty[slot]);
+          }
+          for (int i = 0; i < nb_all && ok; ++i) {
+            if (!(ok = take(vslot))) break;
+            bool have = false;
+            for (int s = 0; s < kStreams && ok; ++s) {
+              if (i < nb[s] && !(ok = issue_pv(s, i, vslot))) break;
+              if (s == kStreams - 1) mma_commit(&rempty[vslot]);
+              if (i + 1 < nb[s]) {
+                if (!have && !(ok = take(slot))) break;
+                have = true;
+                issue_s(s, slot);
               }
             }
-          } else {
-            if ((ok = take(slot))) {
-              for (int s = 0; s < 2; ++s)
-                if (nb[s] > 0) issue_s(s, slot);
-              mma_commit(&rempty[slot]);
-            }
-            for (int i = 0; i < nb_all && ok; ++i) {
-              if (!(ok = take(vslot))) break;
-              bool have = false;
-              for (int s = 0; s < 2 && ok; ++s) {
-                if (i < nb[s] && !(ok = issue_pv(s, i, vslot))) break;
-                if (s == 1) mma_commit(&rempty[vslot]);
-                if (i + 1 < nb[s]) {
-                  if (!have && !(ok = take(slot))) break;
-                  have = true;
-                  issue_s(s, slot);
-                }
-              }
-              if (ok && have) mma_commit(&rempty[slot]);
-            }
+            if (ok && have) mma_commit(&rempty[slot]);
           }
         }
         mma_commit(drain);
@@ -321,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (kSplit)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---------------- softmax and epilogue: stream s, one row per thread
     const int s = (warp - 4) / 4;
     const int quad = warp % 4;
@@ -334,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lim = min(nk, nk - nq + tok + 1);  // keys this row sees
     const bool any_live = quad * 32 < min(a.tpt, nq - t0[s]) * a.G;  // some row of this warp exists
     const int min_lim = nk - nq + t0[s] + 1;                         // keys the tile's first row sees
-    const uint32_t sa = tmem + lane_off + (s ? C::kS1 : C::kS0);
-    const uint32_t oa = tmem + lane_off + (s ? C::kO1 : C::kO0);
+    const uint32_t sa = tmem + lane_off + C::kS + s * 128;
+    const uint32_t oa = tmem + lane_off + C::kO + s * D;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -343,16 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, w);
     };
     for (int j = 0; j < my_nb; ++j) {
-      const int blk = kSplit ? b_lo + 2 * j + s : j;
-      const int k0 = blk * kTile;
+      const int k0 = (b_lo + j) * kTile;
       if (!warp_wait(&sfull[s], j & 1)) { ok = false; break; }
       tc_fence_after();
       if (k0 + kTile > nk) {
         // The keys end inside this block: zero the value rows behind them. The
         // block's ring position follows from the loading order; its copy must
         // have landed first.
-        const int t = 2 * j + s;
-        const int pos = kSplit ? t + min(t + 2, nb_all) : 2 * j + 1;
+        const int pos = 2 * j + 1;
         const int slot = pos % C::kRing;
         if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { ok = false; break; }
         if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
@@ -464,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long rows = (long long)a.Tq * a.Hkv * a.G;
       const long long row = tok_g * a.Hkv * a.G + head;
       if (kSplit) {
-        const long long at = (long long)(2 * z + s) * rows + row;
+        const long long at = (long long)z * rows + row;
         if (live) a.part_l[at] = seen ? m_run + log2f(l_run) : -INFINITY;
         float4* dst = reinterpret_cast<float4*>(a.part_o + at * D);
         if (any_live && have) {
@@ -537,7 +528,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
   const int nq = q_hi - q_lo;
   const int last = min((tok - q_lo) / a.tpt * a.tpt + a.tpt, nq) - 1;
   const int nb = (min(nk, max(0, nk - nq + last + 1)) + kTile - 1) / kTile;
-  const int n = 2 * used_splits(nb, a.nsplit);
+  const int n = used_splits(nb, a.nsplit);
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_l[i * rows + row]);
 #pragma unroll
@@ -583,7 +574,7 @@ Plan plan_of(const vda_attention_config& c) {
   const bool few = (long long)c.Tq <= (long long)c.N * tpt;  // about one tile per sequence
   if (keys >= 2 * kMinSplitBlocks * kTile && (few || (ctas < 148 && keys >= 4 * rows))) {
     p.split = true;
-    const long long want = (148LL * 8 + tiles - 1) / tiles;
+    const long long want = (148LL * kSplitCtas + tiles - 1) / tiles;
     const long long most = std::max(1LL, ((long long)c.Tk + kTile * kMinSplitBlocks - 1) / (kTile * kMinSplitBlocks));
     p.nsplit = (int)std::max(1LL, std::min({want, most, 64LL}));
   }
@@ -594,7 +585,8 @@ template <int D>
 cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K, const void* V, const int* cu_q,
                      const int* cu_k, const int* k_len, void* O, float* lse, void* ws, uint32_t* status,
                      cudaStream_t s) {
-  using C = CaCfg<D>;
+  using C = CaCfg<D, 2>;
+  using C1 = CaCfg<D, 1>;
   const Plan p = plan_of(c);
   CaArgs a{};
   a.N = c.N; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.tpt = kTile / a.G; a.Tq = c.Tq; a.Tk = c.Tk;
@@ -607,7 +599,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   const long long rows = (long long)c.Tq * c.Hq;
   if (p.split) {
     a.part_o = static_cast<float*>(ws);
-    a.part_l = a.part_o + 2LL * p.nsplit * rows * D;
+    a.part_l = a.part_o + (long long)p.nsplit * rows * D;
   }
   a.status = status;
   a.wait_ns = 2000000000u;
@@ -618,7 +610,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const void* fn = p.split ? reinterpret_cast<const void*>(causal_attn_tc_kernel<D, true>)
                            : reinterpret_cast<const void*>(causal_attn_tc_kernel<D, false>);
-  cudaError_t e = set_max_dynamic_smem(fn, C::kSmemBytes);
+  cudaError_t e = set_max_dynamic_smem(fn, p.split ? C1::kSmemBytes : C::kSmemBytes);
   if (e != cudaSuccess) return e;
   uint64_t qdims[3] = {(uint64_t)D, (uint64_t)c.Hq, (uint64_t)c.Tq};
   uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)c.q_row * 2};
@@ -634,11 +626,11 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   if ((e = make_tmap_bf16(&mK, none ? Q : K, 3, kdims, kstr, kbox)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&mV, none ? Q : V, 3, kdims, vstr, kbox)) != cudaSuccess) return e;
   if (p.split) {
-    causal_attn_tc_kernel<D, true><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
+    causal_attn_tc_kernel<D, true><<<(unsigned)grid, C1::kThreads, C1::kSmemBytes, s>>>(mQ, mK, mV, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     attn_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
   } else {
-    causal_attn_tc_kernel<D, false><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
+    causal_attn_tc_kernel<D, false><<<(unsigned)grid, C::kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
   }
   return cudaGetLastError();
 }
@@ -648,7 +640,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
 size_t causal_attention_workspace(const vda_attention_config& c) {
   const Plan p = plan_of(c);
   if (!p.split) return 0;
-  return (size_t)2 * p.nsplit * c.Tq * c.Hq * (c.d + 1) * sizeof(float);
+  return (size_t)p.nsplit * c.Tq * c.Hq * (c.d + 1) * sizeof(float);
 }
 
 cudaError_t launch_causal_attention(const vda_attention_config& c, const void* Q, const void* K, const void* V,
