@@ -770,17 +770,18 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 }
 
 // One token of every sequence: S <- a S + v k^T in place, o = s S q. Memory
-// bound: the state is read and written once. A CTA of four warps takes 32 rows of S
-// (a value channel each), a lane D / 32 key channels of a row; two rows are in flight
-// per warp. Measured at 160 sequences of 24 heads, d = 128 (503 MB): 84.7 us, 5946
+// bound: the state is read and written once. A CTA of four warps takes kSlab rows of
+// S (a value channel each), a lane D / 32 key channels of a row; two rows are in
+// flight per warp. 32 rows to a CTA, or 8 (every row in flight at once) where CTAs
+// are fewer than the SMs hold. Measured at 160 sequences of 24 heads, d = 128 (503 MB): 84.7 us, 5946
 // GB/s; with four rows in flight 90.9, eight warps of four rows to a whole matrix
 // 94.3, eight rows 101: many small CTAs mix reads and writes best.
-template <int D>
+template <int D, int kSlab>
 __global__ void __launch_bounds__(128) decay_step_kernel(const vda_decay_config c, const __nv_bfloat16* Q,
                                                          const __nv_bfloat16* K, const __nv_bfloat16* V,
                                                          const float* log_decay, float* S, __nv_bfloat16* O) {
   constexpr int kPer = D / 32;
-  constexpr int kRows = 2, kSlab = 32, slabs = D / kSlab;
+  constexpr int kRows = 2, slabs = D / kSlab;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int slab = blockIdx.x % slabs;
   const long long nh = blockIdx.x / slabs;
@@ -940,16 +941,19 @@ cudaError_t launch_decay_attention_backward(const vda_decay_config& c, const voi
 
 cudaError_t launch_decay_step(const vda_decay_config& c, const void* Q, const void* K, const void* V,
                               const float* log_decay, float* S, void* O, cudaStream_t s) {
-  const long long grid = (long long)c.N * c.H * (c.d / 32);
+  // Measured with 24 heads, d = 128, 8 (32) rows to a CTA: one sequence 1.9 (3.2) us,
+  // four 2.9 (3.6), eight 4.7 (4.6), 24 9.9 (9.0).
+  const bool few = (long long)c.N * c.H * (c.d / 32) < 148 * 5;
+  const int slab = few ? 8 : 32;
+  const long long grid = (long long)c.N * c.H * (c.d / slab);
   if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
   const auto* q = static_cast<const __nv_bfloat16*>(Q);
   const auto* k = static_cast<const __nv_bfloat16*>(K);
   const auto* v = static_cast<const __nv_bfloat16*>(V);
   auto* o = static_cast<__nv_bfloat16*>(O);
-  if (c.d == 128)
-    decay_step_kernel<128><<<(unsigned)grid, 128, 0, s>>>(c, q, k, v, log_decay, S, o);
-  else
-    decay_step_kernel<64><<<(unsigned)grid, 128, 0, s>>>(c, q, k, v, log_decay, S, o);
+  auto* fn = c.d == 128 ? (few ? decay_step_kernel<128, 8> : decay_step_kernel<128, 32>)
+                        : (few ? decay_step_kernel<64, 8> : decay_step_kernel<64, 32>);
+  fn<<<(unsigned)grid, 128, 0, s>>>(c, q, k, v, log_decay, S, o);
   return cudaGetLastError();
 }
 

@@ -435,7 +435,8 @@ vda_status vda_static_workspace_poll(void* stream);
  * aligned. bf16 storage, d 64 or 128, every sum and state in fp32.
  *
  * These calls take no context and keep no device memory. They only enqueue work;
- * all argument errors come back before any launch. Calls that may run at the
+ * all argument errors come back before any launch. Outputs may not overlap inputs,
+ * but where a call says so. Calls that may run at the
  * same time need separate workspaces. vda_sequence_poll reads the status of
  * their bounded waits.
  */

@@ -66,7 +66,7 @@ def _check_attn(O, lse, ref, n):
     g = f64(lse)[:n]
     assert np.array_equal(np.isneginf(g), np.isneginf(w))
     ok = np.isfinite(w)
-    assert np.abs(g - w)[ok].max(initial=0) <= 2.0 ** -11 + 1e-6 * np.abs(w[ok]).max(initial=0)
+    assert np.abs(g[ok] - w[ok]).max(initial=0) <= 2.0 ** -11 + 1e-6 * np.abs(w[ok]).max(initial=0)
 
 
 @pytest.mark.parametrize("name,Hq,Hkv,d,nq,nk,spread", ATTN, ids=[c[0] for c in ATTN])
@@ -109,7 +109,8 @@ def test_single_tokens_against_a_cache(Hq, Hkv, d, room, lens):
     bounded(f64(O), ref["O"], ref["abs_O"], "O")
     w, g = ref["lse"], f64(lse)
     assert np.array_equal(np.isneginf(g), np.isneginf(w))
-    assert np.abs(g - w)[np.isfinite(w)].max() <= 2.0 ** -11
+    ok = np.isfinite(w)
+    assert np.abs(g[ok] - w[ok]).max() <= 2.0 ** -11
 
 
 def test_causal_attention_of_a_joint_projection_and_of_head_slices():
@@ -230,6 +231,41 @@ def test_decay_attention_backward(name, H, d, lens, scale):
         bounded(f64(out[n]), ref[n], ref["abs_" + n], n)
         assert np.isnan(f64(out[n])[sum(lens):]).all()
     _check_state(f64(out["dS0"]), ref["dS0"], ref["abs_dS0"])
+
+
+def test_decay_attention_backward_without_states():
+    """No initial state, no gradient of the last one, dS0 not wanted."""
+    H, d, lens = 2, 128, [200, 0, 1400]
+    Q, K, Vv, dO, S0, _ = _decay_inputs(H, d, lens)
+    g, zero = slopes(H), np.zeros(S0.shape)
+    ref = po.decay_attention(f64(Q), f64(K), f64(Vv), f64(g), ranges(lens), zero, 1.0, f64(dO), zero)
+    q, k, v, do = (t.to(DEV) for t in (Q, K, Vv, dO))
+    out = {n: torch.full_like(q, float("nan")) for n in ("dQ", "dK", "dV")}
+    V.decay_attention_backward(q, k, v, do, g.to(DEV), starts(lens, DEV), out=out)
+    for n in ("dQ", "dK", "dV"):
+        bounded(f64(out[n]), ref[n], ref["abs_" + n], n)
+
+
+def test_nothing_to_do():
+    """No tokens on one side or on both: gradients of unseen keys are 0, states stay."""
+    H, d = 2, 64
+    x = rand(1, 6, H, d).to(DEV)
+    e = x[:0]
+    none, six = starts([0], DEV), starts([6], DEV)
+    f = dict(device=DEV, dtype=torch.float32)
+    r = V.causal_attention_backward(e, x, x, e, e, torch.empty(0, H, **f), none, cu_k=six)
+    assert (r["dK"] == 0).all() and (r["dV"] == 0).all() and r["dQ"].shape == e.shape
+    O, lse = V.causal_attention(x, e, e, six, cu_k=none, return_lse=True)
+    r = V.causal_attention_backward(x, e, e, O, x, lse, six, cu_k=none)
+    assert (r["dQ"] == 0).all()
+    g, S0 = slopes(H).to(DEV), rand32(3, 1, H, d, d).to(DEV)
+    O, S = V.decay_attention(e, e, e, g, none, S0=S0)
+    assert torch.equal(S, S0) and O.shape == e.shape
+    _, S = V.decay_attention(e, e, e, g, none)
+    assert (S == 0).all()
+    r = V.decay_attention_backward(e, e, e, e, g, none, dS=S0)
+    assert torch.equal(r["dS0"], S0)
+    assert V.decay_attention_step(e, e, e, g, S0[:0]).shape == e.shape
 
 
 @pytest.mark.parametrize("N,H,d", [(1, 1, 128), (1, 24, 128), (3, 5, 64), (70, 8, 128), (300, 2, 64)])
