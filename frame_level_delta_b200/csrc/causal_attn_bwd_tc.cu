@@ -4,15 +4,14 @@
 //   dv_j = sum_r p_rj do_r,   dp_rj = do_r . v_j,   ds_rj = p_rj (dp_rj - D_r),
 //   dq_r = s sum_j ds_rj k_j,   dk_j = s sum_r ds_rj q_r.
 //
-// Three launches. The first writes (lse log2(e), D_r) of every row, in the packed
-// order (key head, token, head of the group) in which tiles take rows. The second
-// gives dK and dV: one CTA per key block of 128, over the query tiles that see it
-// (the group's query heads are rows of the same tile, so their sum is the
-// product's own). The third gives dQ: one CTA per query tile, over its key
-// blocks. Splitting dQ off costs two of seven products (S and dP are formed
+// Two launches. The first writes (lse log2(e), D_r) of every row, in the packed
+// order (key head, token, head of the group) in which tiles take rows. In the second,
+// some CTAs give dK and dV, one per key block of 128, over the query tiles that see
+// it (the group's query heads are rows of the same tile, so their sum is the
+// product's own), and some give dQ, one per query tile, over its key blocks. Splitting dQ off costs two of seven products (S and dP are formed
 // twice) and buys an exact order of summation, no atomics and no fp32 copy of dQ.
 //
-// Second launch, per query tile i (rows = keys, columns = queries):
+// dK and dV, per query tile i (rows = keys, columns = queries):
 //   S^T = K Q_i^T, dP^T = V dO_i^T (operands in shared memory), P^T and dS^T as
 //   bf16 back into the TMEM columns they came from, dV += P^T dO_i,
 //   dK += dS^T Q_i (left operands from TMEM). S and dP of the next tile are issued
@@ -20,7 +19,7 @@
 //   exponentials overlap. Sixteen warps share the elementwise work, a quarter of
 //   the columns each (with eight, a tile's two elementwise phases took 3460 of its
 //   4360 cycles).
-// Third launch, per key block i (rows = queries): S = Q K_i^T into one of two
+// dQ, per key block i (rows = queries): S = Q K_i^T into one of two
 //   buffers, dP = dO V_i^T, dS as bf16 over S, dQ += dS K_i.
 //
 // P and dS are rounded to bf16 for the products (the operand type); everything
@@ -168,15 +167,11 @@ struct CbBars {
 // column (c % 32) / 2 + (c / 32) * 32 of S^T (dP^T): each quarter of the
 // elementwise warps overwrites only columns that it has read itself.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                        const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG,
-                        const CbArgs a) {
+__device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorMap* mK, const CUtensorMap* mV,
+                                          const CUtensorMap* mG, const CbArgs& a, int bid, uint8_t* smem) {
   using C = CbCfg<D>;
   using namespace sm100;
   constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 256 + D;
-  extern __shared__ __align__(1024) uint8_t smem_1024[];
-  uint8_t* smem = smem_1024;
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::kTileBytes;
   uint8_t* sR = smem + C::kRingOff;
@@ -186,20 +181,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 0 && lane == 0) {
     b.init();
-    prefetch_tmap(&mQ);
-    prefetch_tmap(&mK);
-    prefetch_tmap(&mV);
-    prefetch_tmap(&mG);
+    prefetch_tmap(mQ);
+    prefetch_tmap(mK);
+    prefetch_tmap(mV);
+    prefetch_tmap(mG);
   }
   if (warp == 1) {
     tmem_alloc(b.tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
-  const int hk = blockIdx.x % a.Hkv;
+  const int hk = bid % a.Hkv;
   int kb;
   const int sq = seq::find_item(
-      blockIdx.x / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
+      bid / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
       [&](int i) {
         int lo, n;
         key_range(a, i, lo, n);
@@ -250,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(b.own, 2 * C::kTileBytes);
 #pragma unroll
         for (int at = 0; at < C::kAtoms; ++at) {
-          tma_load_3d(sK + at * (kTile * 128), &mK, b.own, at * 64, hk, k_lo + k0);
-          tma_load_3d(sV + at * (kTile * 128), &mV, b.own, at * 64, hk, k_lo + k0);
+          tma_load_3d(sK + at * (kTile * 128), mK, b.own, at * 64, hk, k_lo + k0);
+          tma_load_3d(sV + at * (kTile * 128), mV, b.own, at * 64, hk, k_lo + k0);
         }
       }
       bool ok = true;
@@ -264,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(&b.rfull[slot], (uint32_t)rows * 128u * C::kAtoms);
 #pragma unroll
             for (int at = 0; at < C::kAtoms; ++at)
-              tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), u ? &mG : &mQ, &b.rfull[slot], at * 64,
+              tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), u ? mG : mQ, &b.rfull[slot], at * 64,
                           hk * a.G, q_lo + t0);
           }
           ++issued;
@@ -452,14 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- dQ
 // TMEM: S (two buffers) | dP | dQ. Ring tiles: K_i, V_i.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    attn_dq_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                      const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG, const CbArgs a) {
+__device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap* mK, const CUtensorMap* mV,
+                                        const CUtensorMap* mG, const CbArgs& a, int bid, uint8_t* smem) {
   using C = CbCfg<D>;
   using namespace sm100;
   constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
-  extern __shared__ __align__(1024) uint8_t smem_1024[];
-  uint8_t* smem = smem_1024;
   uint8_t* sQ = smem;
   uint8_t* sG = smem + C::kTileBytes;
   uint8_t* sR = smem + C::kRingOff;
@@ -468,20 +460,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 0 && lane == 0) {
     b.init();
-    prefetch_tmap(&mQ);
-    prefetch_tmap(&mK);
-    prefetch_tmap(&mV);
-    prefetch_tmap(&mG);
+    prefetch_tmap(mQ);
+    prefetch_tmap(mK);
+    prefetch_tmap(mV);
+    prefetch_tmap(mG);
   }
   if (warp == 1) {
     tmem_alloc(b.tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
-  const int hk = blockIdx.x % a.Hkv;
+  const int hk = bid % a.Hkv;
   int idx;
   const int sq = seq::find_item(
-      blockIdx.x / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
+      bid / a.Hkv, a.N, b.scratch, reinterpret_cast<int*>(smem),
       [&](int i) {
         int lo, hi;
         seq::bounds(a.cu_q, i, a.Tq, lo, hi);
@@ -524,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(b.own, 2u * rows * 128u * C::kAtoms);
 #pragma unroll
       for (int at = 0; at < C::kAtoms; ++at) {
-        tma_load_3d(sQ + at * (kTile * 128), &mQ, b.own, at * 64, hk * a.G, q_lo + t0);
-        tma_load_3d(sG + at * (kTile * 128), &mG, b.own, at * 64, hk * a.G, q_lo + t0);
+        tma_load_3d(sQ + at * (kTile * 128), mQ, b.own, at * 64, hk * a.G, q_lo + t0);
+        tma_load_3d(sG + at * (kTile * 128), mG, b.own, at * 64, hk * a.G, q_lo + t0);
       }
       bool ok = true;
       for (int i = 0; i < n_it && ok; ++i)
@@ -535,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&b.rfull[slot], C::kTileBytes);
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
-            tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), u ? &mV : &mK, &b.rfull[slot], at * 64, hk,
+            tma_load_3d(sR + slot * C::kTileBytes + at * (kTile * 128), u ? mV : mK, &b.rfull[slot], at * 64, hk,
                         k_lo + i * kTile);
           ++issued;
         }
@@ -665,6 +657,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Both in one launch: the blocks of dK and dV first, those of dQ fill the SMs as the
+// last of them run out. (One CTA to an SM either way, so an SM runs one role's code.)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                       const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG, const CbArgs a,
+                       const int k_items) {
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  if ((int)blockIdx.x < k_items)
+    attn_dkdv<D>(&mQ, &mK, &mV, &mG, a, blockIdx.x, smem_1024);
+  else
+    attn_dq<D>(&mQ, &mK, &mV, &mG, a, (int)blockIdx.x - k_items, smem_1024);
+}
+
 template <int D>
 cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K, const void* V, const void* O,
                      const void* dO, const float* lse, const int* cu_q, const int* cu_k, const int* k_len, void* dQ,
@@ -685,11 +691,9 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   const long long k_items = ((long long)c.Tk / kTile + c.N) * c.Hkv;
   const long long q_items = ((long long)c.Tq / a.tpt + c.N) * c.Hkv;
   const long long rows = (long long)c.Tq * c.Hq;
-  if (k_items >= (1LL << 31) || q_items >= (1LL << 31) || (rows + 7) / 8 >= (1LL << 31))
+  if (k_items + q_items >= (1LL << 31) || (rows + 7) / 8 >= (1LL << 31))
     return cudaErrorInvalidConfiguration;
-  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_dkdv_tc_kernel<D>), C::kSmemBytes)) != cudaSuccess)
-    return e;
-  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_dq_tc_kernel<D>), C::kSmemBytes)) != cudaSuccess)
+  if ((e = set_max_dynamic_smem(reinterpret_cast<const void*>(attn_bwd_tc_kernel<D>), C::kSmemBytes)) != cudaSuccess)
     return e;
   // An empty side is described by the other: nothing is loaded from it.
   const void* qp = c.Tq ? Q : K;
@@ -714,11 +718,8 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
         static_cast<float2*>(ws), c.Tq, c.Hq, a.G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (c.Tk > 0) {
-    attn_dkdv_tc_kernel<D><<<(unsigned)k_items, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, mG, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  if (c.Tq > 0) attn_dq_tc_kernel<D><<<(unsigned)q_items, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, mG, a);
+  const long long kb = c.Tk > 0 ? k_items : 0, qb = c.Tq > 0 ? q_items : 0;
+  attn_bwd_tc_kernel<D><<<(unsigned)(kb + qb), kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, mG, a, (int)kb);
   return cudaGetLastError();
 }
 

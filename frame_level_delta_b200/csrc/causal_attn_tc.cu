@@ -11,18 +11,17 @@
 // independent in every product, so rows that do not exist (G not dividing 128,
 // tokens past the sequence) carry what lies there and are not stored.
 //
-// Prompts: a CTA runs two streams, two consecutive tiles that share each key block,
-// each with its own four softmax warps, its own logits S and its own accumulator O in
-// TMEM (S 2 x 128 columns, O 2 x D; the probabilities overwrite their logits as
-// packed bf16), so that the tensor cores work on one stream's products while the
-// other's exponentials run.
+// An SM works on two tiles at a time, so that the tensor cores have one's products
+// while the other's exponentials run. Each tile has four softmax warps, its logits S
+// and its accumulator O in TMEM (128 and D columns; the probabilities overwrite their
+// logits as packed bf16). The two are streams of one CTA that share each key block
+// (long prompts at d = 128, where the reads of K and V count), or two CTAs of one
+// stream, so that one's start and end hide behind the other's blocks.
 //
 // Few rows on long keys (single new tokens) are bound by the bytes of K and V, and
-// by how evenly sequences of different lengths fill the SMs: a CTA has one stream and
-// half the shared memory and TMEM, two run on an SM, so that one's start and end hide
-// behind the other's copies, and a tile's key blocks are shared out over several
-// CTAs, each of which leaves a partial (o normalised by its own l, its log-sum) that
-// a second kernel joins.
+// by how evenly sequences of different lengths fill the SMs: there a tile's key
+// blocks are shared out over several CTAs, each of which leaves a partial (o
+// normalised by its own l, its log-sum) that a second kernel joins.
 //
 // Per key block: S = Q K^T (M = 128, N = 128), m = running row maximum in the
 // log2 domain, P = 2^(S s log2(e) - m) rounded to bf16 (the tensor cores' operand
@@ -51,6 +50,7 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kMinSplitBlocks = 4;
 constexpr int kSplitCtas = 8;  // CTAs per SM that the split form aims at
+constexpr int kShortKeys = 1280;  // d = 128: mean keys below which a CTA has one stream
 constexpr uint32_t kFma = 0x92;  // pairs of eight whose exponentials the FMA pipe takes
 
 template <int D, int kStreams>
@@ -59,7 +59,7 @@ struct CaCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
   // Key and value blocks in flight, one ring.
-  static constexpr int kRing = kStreams == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+  static constexpr int kRing = kStreams == 2 || D == 64 ? 5 : 2;
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kStreams * kTileBytes;
   static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
@@ -103,11 +103,10 @@ __device__ __forceinline__ int used_splits(int nb, int nsplit) {
   return max(1, min(nsplit, (nb + kMinSplitBlocks - 1) / kMinSplitBlocks));
 }
 
-template <int D, bool kSplit>
-__global__ void __launch_bounds__((CaCfg<D, kSplit ? 1 : 2>::kThreads), (kSplit ? 2 : 1))
+template <int D, int kStreams, bool kSplit>
+__global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
     causal_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                           const __grid_constant__ CUtensorMap mV, const CaArgs a) {
-  constexpr int kStreams = kSplit ? 1 : 2;
   using C = CaCfg<D, kStreams>;
   using namespace sm100;
   extern __shared__ uint8_t smem_raw[];
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__((CaCfg<D, kSplit ? 1 : 2>::kThreads), (kSplit 
   // most of theirs to the rows' 128 logits (56 + 2 x 224 = 504 = 3 x 168; 48 + 208 =
   // 256 = 2 x 128).
   if (warp < 4) {
-    if constexpr (kSplit)
+    if constexpr (kStreams == 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -311,7 +310,7 @@ __global__ void __launch_bounds__((CaCfg<D, kSplit ? 1 : 2>::kThreads), (kSplit 
     }
     __syncwarp();
   } else {
-    if constexpr (kSplit)
+    if constexpr (kStreams == 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -556,11 +555,19 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
   if (lane == 0 && a.lse) a.lse[row] = m > -INFINITY ? (m + log2f(w_all)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The form and the number of key shares for a call. Prompts fill the GPU with
-// tiles; where two-tile CTAs are fewer than the SMs and the keys are longer than
-// the rows are many, the keys are shared out instead, in enough shares to give
-// each SM several CTAs (sequences differ in length, and a CTA takes one share).
+// The form and the number of key shares for a call, by mean lengths (the lengths
+// themselves are on the device).
+//  - Few rows on long keys: one stream a CTA, the keys shared out, in enough shares
+//    to give each SM several CTAs.
+//  - d = 64, and short sequences at d = 128: one stream a CTA, two CTAs to an SM: one's
+//    start and end hide behind the other's blocks.
+//  - Else two streams a CTA, which halves the reads of K and V.
+// Measured at d = 128, 24 / 8 heads, one stream (two): 16 x 256 tokens 34.8 (40.1) us,
+// 16 x 512 77.5 (83.1), 8 x 1024 97.8 (99.7), 8 x 1536 173 (170), 4 x 3000 264 (243),
+// 2 x 4096 229 (207); at d = 64, 8 / 8 heads: 16 x 512 23.7 (26.4), 8 x 1536 54.9
+// (59.8), 2 x 4096 64.9 (66.3).
 struct Plan {
+  int streams;
   bool split;
   int nsplit;
 };
@@ -569,10 +576,11 @@ Plan plan_of(const vda_attention_config& c) {
   const long long tiles = ((long long)c.Tq / tpt + c.N) * c.Hkv;
   const long long ctas = ((long long)c.Tq / (2 * tpt) + (c.N + 1) / 2) * c.Hkv;
   const long long keys = (long long)c.Tk / c.N;  // mean room per sequence
-  Plan p{false, 1};
   const long long rows = (long long)c.Tq / c.N;
   const bool few = (long long)c.Tq <= (long long)c.N * tpt;  // about one tile per sequence
+  Plan p{few || c.d == 64 || keys < kShortKeys ? 1 : 2, false, 1};
   if (keys >= 2 * kMinSplitBlocks * kTile && (few || (ctas < 148 && keys >= 4 * rows))) {
+    p.streams = 1;
     p.split = true;
     const long long want = (148LL * kSplitCtas + tiles - 1) / tiles;
     const long long most = std::max(1LL, ((long long)c.Tk + kTile * kMinSplitBlocks - 1) / (kTile * kMinSplitBlocks));
@@ -585,7 +593,6 @@ template <int D>
 cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K, const void* V, const int* cu_q,
                      const int* cu_k, const int* k_len, void* O, float* lse, void* ws, uint32_t* status,
                      cudaStream_t s) {
-  using C = CaCfg<D, 2>;
   using C1 = CaCfg<D, 1>;
   const Plan p = plan_of(c);
   CaArgs a{};
@@ -603,14 +610,22 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   }
   a.status = status;
   a.wait_ns = 2000000000u;
-  const int per_item = p.split ? a.tpt : 2 * a.tpt;
+  const int per_item = p.streams * a.tpt;
   // ceil(n / per_item) summed over the sequences is at most Tq / per_item + N.
   const long long items = (long long)c.Tq / per_item + c.N;
   const long long grid = items * c.Hkv * p.nsplit;
   if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-  const void* fn = p.split ? reinterpret_cast<const void*>(causal_attn_tc_kernel<D, true>)
-                           : reinterpret_cast<const void*>(causal_attn_tc_kernel<D, false>);
-  cudaError_t e = set_max_dynamic_smem(fn, p.split ? C1::kSmemBytes : C::kSmemBytes);
+  auto* fn = p.split ? causal_attn_tc_kernel<D, 1, true> : causal_attn_tc_kernel<D, 1, false>;
+  int threads = C1::kThreads, smem = C1::kSmemBytes;
+  if constexpr (D == 128) {
+    using C2 = CaCfg<D, 2>;
+    if (p.streams == 2) {
+      fn = causal_attn_tc_kernel<D, 2, false>;
+      threads = C2::kThreads;
+      smem = C2::kSmemBytes;
+    }
+  }
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(fn), smem);
   if (e != cudaSuccess) return e;
   uint64_t qdims[3] = {(uint64_t)D, (uint64_t)c.Hq, (uint64_t)c.Tq};
   uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)c.q_row * 2};
@@ -625,13 +640,10 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   if ((e = make_tmap_bf16(&mQ, Q, 3, qdims, qstr, qbox)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&mK, none ? Q : K, 3, kdims, kstr, kbox)) != cudaSuccess) return e;
   if ((e = make_tmap_bf16(&mV, none ? Q : V, 3, kdims, vstr, kbox)) != cudaSuccess) return e;
-  if (p.split) {
-    causal_attn_tc_kernel<D, true><<<(unsigned)grid, C1::kThreads, C1::kSmemBytes, s>>>(mQ, mK, mV, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
-  } else {
-    causal_attn_tc_kernel<D, false><<<(unsigned)grid, C::kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, a);
-  }
+  fn<<<(unsigned)grid, threads, smem, s>>>(mQ, mK, mV, a);
+  if (!p.split) return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  attn_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
