@@ -74,6 +74,19 @@ __device__ __forceinline__ void key_range(const CbArgs& a, int i, int& lo, int& 
   if (a.k_len) n = min(n, max(__ldg(a.k_len + i), 0));
 }
 
+// Token and query head of a row; 32-bit division where the row allows it (a 64-bit one
+// costs more than the row's loads).
+__device__ __forceinline__ void split_row(long long row, int Hq, long long& tok, int& h) {
+  if (row < (1LL << 31)) {
+    const unsigned t = (unsigned)row / (unsigned)Hq;
+    tok = t;
+    h = (int)((unsigned)row - t * (unsigned)Hq);
+  } else {
+    tok = row / Hq;
+    h = (int)(row % Hq);
+  }
+}
+
 // D / 8 threads per row (token, query head), 16 bytes each; kPerThread rows in
 // flight per thread.
 template <int D>
@@ -85,11 +98,14 @@ __global__ void __launch_bounds__(256) attn_rowdot_kernel(const __nv_bfloat16* O
   const long long rows = (long long)Tq * Hq;
   const long long row0 = (long long)blockIdx.x * (kRows * kPerThread) + threadIdx.x / kLanes;
   uint4 x[kPerThread], y[kPerThread];
+  long long tok;
+  int h;
 #pragma unroll
   for (int u = 0; u < kPerThread; ++u) {
     const long long row = row0 + u * kRows;
     if (row < rows) {
-      const long long at = row / Hq * o_row + row % Hq * D + part * 8;
+      split_row(row, Hq, tok, h);
+      const long long at = tok * o_row + h * D + part * 8;
       x[u] = __ldcs(reinterpret_cast<const uint4*>(O + at));
       y[u] = __ldg(reinterpret_cast<const uint4*>(dO + at));
     }
@@ -109,8 +125,7 @@ __global__ void __launch_bounds__(256) attn_rowdot_kernel(const __nv_bfloat16* O
 #pragma unroll
     for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (part == 0 && row < rows) {
-      const long long tok = row / Hq;
-      const int h = (int)(row % Hq);
+      split_row(row, Hq, tok, h);
       stat[((long long)(h / G) * Tq + tok) * G + h % G] = make_float2(lse[row] * 1.4426950408889634f, s);
     }
   }
