@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(256) attn_rowdot_kernel(const __nv_bfloat16* O
                                                           long long o_row, const float* lse, float2* stat, int Tq,
                                                           int Hq, int G) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes, kPerThread = 4;
+  seq::grid_trigger();
   const int part = threadIdx.x % kLanes;
   const long long rows = (long long)Tq * Hq;
   const long long row0 = (long long)blockIdx.x * (kRows * kPerThread) + threadIdx.x / kLanes;
@@ -216,7 +217,9 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
         return n;
       },
       [&](int n) { return (n + kTile - 1) / kTile; }, kb);
-  if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
+  seq::grid_wait();
+  if (sq < 0) {
+    __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);
     return;
@@ -237,7 +240,7 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
   for (int r = rows + (int)threadIdx.x; r < kTile; r += kThreads)
     for (int t = 0; t < C::kRing; ++t) seq::zero_row(sR + t * C::kTileBytes, C::kAtoms, r, kTile);
   fence_proxy_async_smem();
-  __syncthreads();
+  seq::set_up(warp == 0);
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   int issued = 0;
@@ -495,7 +498,9 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
         return hi - lo;
       },
       [&](int n) { return (n + a.tpt - 1) / a.tpt; }, idx);
-  if (sq < 0) {  // (the list's search synchronises the block behind the set-up above)
+  seq::grid_wait();
+  if (sq < 0) {
+    __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(*b.tmem_slot, C::kTmemCols);
     return;
@@ -511,6 +516,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
   const int n_it = (min(nk, max(0, shift + last + 1)) + kTile - 1) / kTile;
   const int rows = a.tpt * a.G;
 
+  seq::set_up(warp == 0);
   tc_fence_after();
   const uint32_t tmem = *b.tmem_slot;
   int issued = 0;
@@ -680,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG, const CbArgs a,
                        const int k_items) {
   extern __shared__ __align__(1024) uint8_t smem_1024[];
+  // (The waits for the rows' statistics stand before each one's first way out.)
   if ((int)blockIdx.x < k_items)
     attn_dkdv<D>(&mQ, &mK, &mV, &mG, a, blockIdx.x, smem_1024);
   else
@@ -734,7 +741,10 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const long long kb = c.Tk > 0 ? k_items : 0, qb = c.Tq > 0 ? q_items : 0;
-  attn_bwd_tc_kernel<D><<<(unsigned)(kb + qb), kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, mG, a, (int)kb);
+  if (rows > 0)
+    return seq::launch_behind(attn_bwd_tc_kernel<D>, dim3((unsigned)(kb + qb)), kThreads, C::kSmemBytes, s, mQ, mK, mV,
+                              mG, a, (int)kb);
+  attn_bwd_tc_kernel<D><<<(unsigned)kb, kThreads, C::kSmemBytes, s>>>(mQ, mK, mV, mG, a, (int)kb);
   return cudaGetLastError();
 }
 

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
   int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
   static_assert((1 + 2 * C::kRing + 9) * 8 + 16 + 160 <= 512, "barrier block overflows its allowance");
 
+  if (kSplit) seq::grid_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 0 && lane == 0) {
     mbar_init(qfull, 1);
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
         return hi - lo;
       },
       [&](int n) { return (n + per_item - 1) / per_item; }, idx);
-  // (The list's search synchronises the block behind the set-up above.)
   auto leave = [&] {
+    __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(*tmem_slot, C::kTmemCols);
   };
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
   }
   const int nb_all = max(nb[0], nb[1]);
 
+  seq::set_up(kStreams == 1 && warp == 0);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -511,9 +513,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
   const long long rows = (long long)a.Tq * Hq;
   const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  if (row >= rows) return;
   const int tok = (int)(row / Hq), head = (int)(row % Hq);
-  if (tok < __ldg(a.cu_q) || tok >= __ldg(a.cu_q + a.N)) return;  // behind the last sequence: left as it was
+  // Rows outside the sequences are left as they were.
+  if (row >= rows || tok < __ldg(a.cu_q) || tok >= __ldg(a.cu_q + a.N)) {
+    seq::grid_wait();
+    return;
+  }
   // The row's sequence: the last one that starts at or before it.
   int lo = 0, hi = a.N - 1;
   while (lo < hi) {
@@ -528,6 +533,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
   const int last = min((tok - q_lo) / a.tpt * a.tpt + a.tpt, nq) - 1;
   const int nb = (min(nk, max(0, nk - nq + last + 1)) + kTile - 1) / kTile;
   const int n = used_splits(nb, a.nsplit);
+  seq::grid_wait();
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_l[i * rows + row]);
 #pragma unroll
@@ -643,8 +649,7 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   fn<<<(unsigned)grid, threads, smem, s>>>(mQ, mK, mV, a);
   if (!p.split) return cudaGetLastError();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attn_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return seq::launch_behind(attn_join_kernel<D>, dim3((unsigned)((rows + 7) / 8)), 256, 0, s, a);
 }
 
 }  // namespace

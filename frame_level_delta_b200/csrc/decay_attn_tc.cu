@@ -132,9 +132,15 @@ __device__ __forceinline__ void chunk_tokens(int len, int reverse, int p0, int p
 }
 
 // Segments of the sequences before sequence sq: where its own begin in seg_state.
-// Every thread of the block calls it.
+// Every thread of the block calls it; up to 32 sequences each warp counts by itself.
 __device__ __forceinline__ int segments_before(const DaArgs& a, int sq, int* scratch) {
   const int seg_tokens = a.seg * kC;
+  if (a.N <= 32) {
+    int lo = 0, hi = 0;
+    const int lane = threadIdx.x % 32;
+    if (lane < sq) seq::bounds(a.cu, lane, a.T, lo, hi);
+    return (int)__reduce_add_sync(0xffffffffu, lane < sq ? max(1, (hi - lo + seg_tokens - 1) / seg_tokens) : 0);
+  }
   if (threadIdx.x == 0) *scratch = 0;
   __syncthreads();
   int n = 0;
@@ -213,12 +219,43 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   float* wt = pw + 96;                                 // [256] weights of V' in a whole chunk, then zeros
   static_assert((23 + 2 * kMakers) * 8 + 16 + 160 + 4 * (96 + 256) + 16 <= 2048, "barrier block overflows its allowance");
 
+  if (kStateOnly) seq::grid_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int jb = blockIdx.x % a.njobs;
   const int h = (blockIdx.x / a.njobs) % a.H;
   const int item = blockIdx.x / a.njobs / a.H;
   const DaJob& job = a.job[jb];
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 2);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    if (!kStateOnly) prefetch_tmap(&maps.m[job.q]);
+    prefetch_tmap(&maps.m[job.k]);
+    prefetch_tmap(&maps.m[job.v]);
+  }
+  if (warp == 1 && lane == 0) {
+    mbar_init(sfull, 1);
+    mbar_init(pfull, 8);
+    mbar_init(qxdone, 1);
+    mbar_init(odone, 1);
+    mbar_init(oempty, 8);
+    for (int i = 0; i < kMakers; ++i) {
+      mbar_init(&vpfull[i], 4);
+      mbar_init(&vpempty[i], 1);
+    }
+    mbar_init(wfull, 1);
+    mbar_init(wempty, 8);
+    mbar_init(xfull, 8);
+    mbar_init(ofull, 8);
+    mbar_init(drain, 2);
+    *v_read = 0;
+    fence_mbar_init();
+  }
   const int seg_tokens = a.seg * kC;
+  const float g2 = head_decay(a, h);
   int part;
   // An empty sequence still has a state. The launch that forms states leaves out a
   // sequence's last segment: nothing follows it.
@@ -230,7 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         return hi - lo;
       },
       [&](int n) { return max(1, (n + seg_tokens - 1) / seg_tokens) - (kStateOnly ? 1 : 0); }, part);
-  if (sq < 0) return;
+  if (sq < 0) {
+    if (!kStateOnly) seq::grid_wait();
+    return;
+  }
   int lo, hi;
   seq::bounds(a.cu, sq, a.T, lo, hi);
   const int len = hi - lo;
@@ -238,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
   const int p0 = part * a.seg, nch = min(nch_all, p0 + a.seg) - p0;
   const int rev = job.reverse;
-  const float g2 = head_decay(a, h);
   const long long st_off = ((long long)sq * a.H + h) * (D * D);
   float* seg_state = nullptr;
   if (a.seg_state && nparts > 1) {
@@ -258,32 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   auto slot_of = [&](int c, int t) { return kStateOnly ? c % 3 * 2 + t - 1 : (c & 1) * 3 + t; };
   auto tile_of = [&](int c, int t) { return smem + slot_of(c, t) * C::kTileBytes; };
 
-  if (warp == 0 && lane == 0) {
-    for (int i = 0; i < 6; ++i) {
-      mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 2);
-    }
-    mbar_init(sfull, 1);
-    mbar_init(pfull, 8);
-    mbar_init(qxdone, 1);
-    mbar_init(odone, 1);
-    mbar_init(oempty, 8);
-    for (int i = 0; i < kMakers; ++i) {
-      mbar_init(&vpfull[i], 4);
-      mbar_init(&vpempty[i], 1);
-    }
-    mbar_init(wfull, 1);
-    mbar_init(wempty, 8);
-    mbar_init(xfull, 8);
-    mbar_init(ofull, 8);
-    mbar_init(drain, 2);
-    *abort_flag = 0;
-    *v_read = 0;
-    fence_mbar_init();
-    if (!kStateOnly) prefetch_tmap(&maps.m[job.q]);
-    prefetch_tmap(&maps.m[job.k]);
-    prefetch_tmap(&maps.m[job.v]);
-  }
   // The weight of a pair is a power of the row's distance from the near edge of a
   // block of 32 columns times one of the column's distance from that edge; on the
   // diagonal, where the two would overflow apart, one power of their distance, 0
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  seq::set_up(warp == 0);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int loaded = 0;  // chunks whose copies have been issued
@@ -623,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       const bool joined = !kStateOnly && nparts > 1;
       const float* src = kStateOnly ? nullptr : joined ? seg_state : job.init ? job.init + st_off : nullptr;
       const bool tr = !joined && job.init_t;
+      if (!kStateOnly) seq::grid_wait();
 #pragma unroll
       for (int k = 0; k < kCols; ++k) X[k] = 0.f;
       if (src && has_row) {
@@ -694,9 +708,23 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     }
     float* last = kStateOnly ? seg_state : (part == nparts - 1 && job.last) ? job.last + st_off : nullptr;
     if (ok && last && has_row) {
+      // Through shared memory, so that a warp's store takes whole lines (straight from
+      // the rows' threads it took 3 us at d = 128): 32 rows of 16-byte pieces, swizzled
+      // by the row, in the Q and K slots that the last chunk has not used. What used
+      // them is done: W of the last chunk, which comes behind, has been read.
+      constexpr int kPieces = kCols / 4, kRows = 32 / kPieces;
+      uint8_t* st = smem + slot_of(nch, kStateOnly ? 1 : 0) * C::kTileBytes +
+                    (half * (D / 32) + quad) * (32 * kCols * 4);
 #pragma unroll
-      for (int k = 0; k < kCols; k += 4)
-        *reinterpret_cast<float4*>(last + row * D + half * kCols + k) = make_float4(X[k], X[k + 1], X[k + 2], X[k + 3]);
+      for (int k = 0; k < kPieces; ++k)
+        *reinterpret_cast<float4*>(st + lane * (kCols * 4) + ((k ^ (lane % kPieces)) * 16)) =
+            make_float4(X[4 * k], X[4 * k + 1], X[4 * k + 2], X[4 * k + 3]);
+      __syncwarp();
+      const int piece = lane % kPieces;
+#pragma unroll 4
+      for (int r = lane / kPieces; r < 32; r += kRows)
+        *reinterpret_cast<float4*>(last + (quad * 32 + r) * D + half * kCols + piece * 4) =
+            *reinterpret_cast<const float4*>(st + r * (kCols * 4) + ((piece ^ (r % kPieces)) * 16));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -723,6 +751,8 @@ template <int D>
 __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DaArgs a) {
   constexpr int kBatch = 8;
   __shared__ int scratch;
+  seq::grid_trigger();
+  seq::grid_wait();
   const int sq = blockIdx.y;
   const int jb = blockIdx.x % a.njobs, h = (blockIdx.x / a.njobs) % a.H;
   const int slice = blockIdx.x / a.njobs / a.H;
@@ -844,14 +874,19 @@ __global__ void __launch_bounds__(128) decay_step_kernel(const vda_decay_config 
 }
 
 constexpr int kMinSegChunks = 4;
+constexpr int kWholeChunks = 9;
 
 // Chunks per segment: one SM's share of the whole work, so that a long sequence
 // is cut into about as many CTAs as there are SMs, but not into less than
 // kMinSegChunks (a segment reads its keys and values twice, and the launch that
-// forms the segments' states costs its start).
+// forms the segments' states costs its start). Up to kWholeChunks in all, nothing is
+// cut: the two launches more cost what the shorter chain saves (one sequence of 24
+// heads, d = 128, in segments of 4: 6 chunks 37 us, 12 chunks 39; uncut 26 and 42; at
+// d = 64 27 and 28 against 20 and 33).
 int segment_chunks(const vda_decay_config& c, int njobs) {
-  const long long chunks = ((long long)c.T + kC - 1) / kC + c.N / 2;
-  const long long share = (chunks * c.H * njobs + 147) / 148;
+  const long long chunks = ((long long)c.T + kC - 1) / kC;
+  if (chunks <= kWholeChunks) return kWholeChunks;
+  const long long share = ((chunks + c.N / 2) * c.H * njobs + 147) / 148;
   return (int)std::min<long long>(1 << 20, std::max<long long>(kMinSegChunks, share));
 }
 long long segment_items(const vda_decay_config& c, int seg) { return (long long)c.T / ((long long)seg * kC) + c.N; }
@@ -890,8 +925,8 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
     decay_attn_tc_kernel<D, true><<<(unsigned)states, kThreads, C::kSmemBytes, s>>>(maps, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const dim3 jg((unsigned)(c.H * a.njobs * (D * D / 1024)), (unsigned)c.N);
-    decay_join_kernel<D><<<jg, 256, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = seq::launch_behind(decay_join_kernel<D>, jg, 256, 0, s, a)) != cudaSuccess) return e;
+    return seq::launch_behind(decay_attn_tc_kernel<D, false>, dim3((unsigned)grid), kThreads, C::kSmemBytes, s, maps, a);
   }
   decay_attn_tc_kernel<D, false><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(maps, a);
   return cudaGetLastError();

@@ -23,14 +23,31 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int T, int& lo, int
 // sequence i's tokens): returns the sequence and x's index within it, or -1 past the
 // list's end. Up to kSorted sequences, the largest come first, so that no long one
 // starts when the others are done; beyond, in their order. Every thread of the block
-// calls it; `scratch` holds 40 ints, `big` 2 kSorted. Each pass takes blockDim.x
-// sequences (one load and one scan), so up to that many cost one pass.
+// calls it; `scratch` holds 40 ints, `big` 2 kSorted. Up to 32 sequences each warp
+// finds the item by itself, so the warp that loads can start at once (a search by the
+// block cost 2 us of a CTA's start, its code's first execution and four barriers); beyond,
+// each pass takes blockDim.x sequences (one load and one scan). The caller
+// synchronises the block.
 constexpr int kSorted = 128;
 template <typename Size, typename Count>
 __device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, Size size, Count count, int& idx) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
+  if (N <= 32) {
+    const int own = lane < N ? size(lane) : 0, c = lane < N ? count(own) : 0;
+    int lo = 0;  // items of the sequences before this lane's
+#pragma unroll 4
+    for (int j = 0; j < N; ++j) {
+      const int s = __shfl_sync(0xffffffffu, own, j), n = __shfl_sync(0xffffffffu, c, j);
+      lo += s > own || (s == own && j < lane) ? n : 0;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < N && x >= lo && x - lo < c);
+    if (hit == 0) return -1;
+    const int sq = __ffs(hit) - 1;
+    idx = x - __shfl_sync(0xffffffffu, lo, sq);
+    return sq;
+  }
   if (t == 0) scratch[33] = -1;
-  const bool sorted = N > 1 && N <= kSorted;
+  const bool sorted = N <= kSorted;
   int own = 0;
   if (sorted) {
     if (t < N) big[t] = own = size(t);
@@ -73,6 +90,41 @@ __device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, S
   __syncthreads();
   idx = scratch[34];
   return scratch[33];
+}
+
+// Of a call's launches, each after the first starts as the programmatic dependent of
+// the one before it: its launch and set-up run under the other's end. The first
+// starts in stream order, so what a call reads is complete for all of them. Every CTA
+// of the others waits (grid_wait: until the launch before has ended and its writes are
+// there) before it ends, or a later kernel of the stream could find an earlier launch
+// still running.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P>
+cudaError_t launch_behind(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                          const P&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// End of a CTA's set-up: every warp waits for it but the one that loads (`first`),
+// whose copies need nothing that the others set up.
+__device__ __forceinline__ void set_up(bool first) {
+  if (first) {
+    __syncwarp();
+    asm volatile("bar.arrive 7, %0;" ::"r"(blockDim.x) : "memory");
+  } else {
+    asm volatile("bar.sync 7, %0;" ::"r"(blockDim.x) : "memory");
+  }
 }
 
 // One lane of a converged warp, chosen by the hardware.
