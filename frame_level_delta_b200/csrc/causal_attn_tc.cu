@@ -12,8 +12,9 @@
 // tokens past the sequence) carry what lies there and are not stored.
 //
 // An SM works on two tiles at a time, so that the tensor cores have one's products
-// while the other's exponentials run. Each tile has four softmax warps, its logits S
-// and its accumulator O in TMEM (128 and D columns; the probabilities overwrite their
+// while the other's exponentials run. Each tile has eight softmax warps (two threads to
+// a row, half the keys each; with four warps a packed batch took 6% longer), its logits
+// S and its accumulator O in TMEM (128 and D columns; the probabilities overwrite their
 // logits as packed bf16). The two are streams of one CTA that share each key block
 // (long prompts at d = 128, where the reads of K and V count), or two CTAs of one
 // stream, so that one's start and end hide behind the other's blocks.
@@ -50,12 +51,12 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kMinSplitBlocks = 4;
 constexpr int kSplitCtas = 8;  // CTAs per SM that the split form aims at
-constexpr int kShortKeys = 1280;  // d = 128: mean keys below which a CTA has one stream
-constexpr uint32_t kFma = 0x92;  // pairs of eight whose exponentials the FMA pipe takes
+constexpr int kShortKeys = 2304;  // d = 128: mean keys below which a CTA has one stream
+constexpr uint32_t kFma = 0x22;  // pairs of eight whose exponentials the FMA pipe takes
 
 template <int D, int kStreams>
 struct CaCfg {
-  static constexpr int kThreads = 128 + 128 * kStreams;  // TMA warp, MMA warp, two idle ones, four warps a stream
+  static constexpr int kThreads = 128 + 256 * kStreams;  // TMA warp, MMA warp, two idle ones, eight warps a stream
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
   // Key and value blocks in flight, one ring.
@@ -63,7 +64,8 @@ struct CaCfg {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kStreams * kTileBytes;
   static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
-  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static constexpr int kPairOff = kBarOff + 512;  // per stream, half and row: what a row's two threads exchange
+  static constexpr int kSmemBytes = kPairOff + kStreams * 1024;  // the array is declared 1024-byte aligned
   static constexpr uint32_t kS = 0, kO = 128 * kStreams;  // stream s: + 128 s, + D s columns
   static constexpr uint32_t kTmemCols = kStreams == 2 ? 512 : 256;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
@@ -109,15 +111,15 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
                           const __grid_constant__ CUtensorMap mV, const CaArgs a) {
   using C = CaCfg<D, kStreams>;
   using namespace sm100;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem_1024[];
+  uint8_t* smem = smem_1024;
   uint8_t* sQ = smem + C::kQOff;
   uint8_t* sR = smem + C::kRingOff;
   uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* rfull = qfull + 1;
   uint64_t* rempty = rfull + C::kRing;
   uint64_t* sfull = rempty + C::kRing;  // [2] logits of stream s in TMEM
-  uint64_t* pfull = sfull + 2;          // [2][2] halves of the probabilities of stream s in TMEM
+  uint64_t* pfull = sfull + 2;          // [2][2] weights of stream s in TMEM: first (second) 32 keys of each half
   uint64_t* pvdone = pfull + 4;         // [2] O of stream s accumulated
   uint64_t* drain = pvdone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -135,8 +137,8 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[2 * i], 4);
-      mbar_init(&pfull[2 * i + 1], 4);
+      mbar_init(&pfull[2 * i], 8);
+      mbar_init(&pfull[2 * i + 1], 8);
       mbar_init(&pvdone[i], 1);
     }
     mbar_init(drain, 1);
@@ -204,14 +206,13 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // 384 (256) threads start with 168 (128) registers each; the first four warps give
-  // most of theirs to the rows' 128 logits (56 + 2 x 224 = 504 = 3 x 168; 48 + 208 =
-  // 256 = 2 x 128).
+  // 640 (384) threads start with 96 (80) registers each; the first four warps give some
+  // of theirs to the others (4 x 64 + 16 x 104 = 20 x 96; 4 x 48 + 8 x 96 = 12 x 80).
   if (warp < 4) {
     if constexpr (kStreams == 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // ---------------- TMA producer. Ring order is the order in which the MMA
       // warp takes blocks: K0, then V_t and the next K in turn.
@@ -274,13 +275,15 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
         auto issue_pv = [&](int s, int j, int slot) -> bool {
           const uint64_t dv = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), kTile * 128, 1024);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!seq::bar_wait(&pfull[2 * s + half], j & 1, abort_flag, a.status, a.wait_ns)) return false;
+          for (int u = 0; u < 2; ++u) {
+            if (!seq::bar_wait(&pfull[2 * s + u], j & 1, abort_flag, a.status, a.wait_ns)) return false;
             tc_fence_after();
 #pragma unroll
-            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-              mma_f16_ts(tmem + C::kO + s * D, tmem + C::kS + s * 128 + kk * 8, dv + kk * 128, C::kIdescO,
-                         (j > 0 || kk > 0) ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) {
+              const int half = k / 2, kk = half * 4 + u * 2 + k % 2;
+              mma_f16_ts(tmem + C::kO + s * D, tmem + C::kS + s * 128 + half * 64 + (u * 2 + k % 2) * 8, dv + kk * 128,
+                         C::kIdescO, (j > 0 || u + k > 0) ? 1u : 0u);
+            }
           }
           mma_commit(&pvdone[s]);
           return true;
@@ -313,11 +316,12 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
     __syncwarp();
   } else {
     if constexpr (kStreams == 1)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // ---------------- softmax and epilogue: stream s, one row per thread
-    const int s = (warp - 4) / 4;
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---------------- softmax and epilogue: stream s, a row to two threads, half the
+    // keys (channels) each
+    const int s = (warp - 4) / 8, half = (warp - 4) / 4 % 2;
     const int quad = warp % 4;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -326,65 +330,86 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
     const int head = hk * a.G + r % a.G;
     const bool live = r < a.tpt * a.G && tok < nq;
     const int lim = min(nk, nk - nq + tok + 1);  // keys this row sees
+    const int warp_lim = __shfl_sync(0xffffffffu, lim, 31);  // and any row of this warp
     const bool any_live = quad * 32 < min(a.tpt, nq - t0[s]) * a.G;  // some row of this warp exists
     const int min_lim = nk - nq + t0[s] + 1;                         // keys the tile's first row sees
-    const uint32_t sa = tmem + lane_off + C::kS + s * 128;
-    const uint32_t oa = tmem + lane_off + C::kO + s * D;
+    const uint32_t sa = tmem + lane_off + C::kS + s * 128 + half * 64;
+    const uint32_t oa = tmem + lane_off + C::kO + s * D + half * (D / 2);
+    volatile float* mine = reinterpret_cast<float*>(smem + C::kPairOff) + (s * 2 + half) * kTile + r;
+    volatile float* other = reinterpret_cast<float*>(smem + C::kPairOff) + (s * 2 + 1 - half) * kTile + r;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       const bool w = seq::bar_wait(bar, parity, abort_flag, a.status, a.wait_ns);
       return __all_sync(0xffffffffu, w);
     };
+    // The two warps of 32 rows meet, and go on if no wait has given up. A warp that goes no
+    // further arrives once more (fail), so that the other, which sees the flag behind the
+    // barrier, never waits for it.
+    const int pair = 1 + s * 4 + quad;
+    auto meet = [&]() -> bool {
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      return !__any_sync(0xffffffffu, *abort_flag != 0);
+    };
+    auto fail = [&] {
+      ok = false;
+      __syncwarp();
+      asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
+    };
     for (int j = 0; j < my_nb; ++j) {
       const int k0 = (b_lo + j) * kTile;
-      if (!warp_wait(&sfull[s], j & 1)) { ok = false; break; }
+      const int kh = k0 + half * 64;  // this thread's first key
+      if (!warp_wait(&sfull[s], j & 1)) { fail(); break; }
       tc_fence_after();
-      if (k0 + kTile > nk) {
+      if (k0 + kTile > nk && half == 0) {
         // The keys end inside this block: zero the value rows behind them. The
         // block's ring position follows from the loading order; its copy must
         // have landed first.
         const int pos = 2 * j + 1;
         const int slot = pos % C::kRing;
-        if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { ok = false; break; }
+        if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { fail(); break; }
         if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
         fence_proxy_async_smem();
       }
       if (any_live) {
-        float x[kTile];
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t v[32];
-          seq::tmem_ld32(sa + c4 * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[c4 * 32 + k] = __uint_as_float(v[k]);
-        }
         const bool masked = k0 + kTile > min_lim;
-        if (masked) {
-          const int n = lim - k0;
+        const int n = lim - kh;  // keys of this half that the row sees
+        // Logits are read twice, for the maximum and for the weights: kept, they would
+        // leave no registers to work with.
+        float mb = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < kTile; ++k)
-            if (k >= n) x[k] = -INFINITY;
+        for (int c2 = 0; c2 < 2; ++c2) {
+          uint32_t v[32];
+          seq::tmem_ld32(sa + c2 * 32, v);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c2 * 32 + k >= n) v[k] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(v[q]);
+#pragma unroll
+          for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
+          mb = fmaxf(mb, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         }
-        float mx[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) mx[q] = x[q];
-#pragma unroll
-        for (int k = 8; k < kTile; ++k) mx[k & 7] = fmaxf(mx[k & 7], x[k]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], mx[q + 4]);
-        const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl;
+        mb *= a.sl;
+        // (The other thread has read the last block's: the product that this block's
+        // logits came behind waited for its probabilities.)
+        *mine = mb;
+        if (!meet()) { fail(); break; }
+        mb = fmaxf(mb, *other);
         const bool grow = j > 0 && mb > m_run + 8.f;
         if (j == 0) m_run = mb;
         if (__any_sync(0xffffffffu, grow)) {
-          if (!warp_wait(&pvdone[s], (j - 1) & 1)) { ok = false; break; }
+          if (!warp_wait(&pvdone[s], (j - 1) & 1)) { fail(); break; }
           tc_fence_after();
           const float f = grow ? seq::ex2_approx(m_run - mb) : 1.f;
 #pragma unroll
-          for (int c4 = 0; c4 < D / 32; ++c4) {
+          for (int c2 = 0; c2 < D / 64; ++c2) {
             uint32_t v[32];
-            seq::tmem_ld32(oa + c4 * 32, v);
+            seq::tmem_ld32(oa + c2 * 32, v);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
@@ -393,7 +418,7 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
               uint32_t w[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) w[k] = v[q * 16 + k];
-              tmem_st16(oa + c4 * 32 + q * 16, w);
+              tmem_st16(oa + c2 * 32 + q * 16, w);
             }
           }
           if (grow) {
@@ -407,25 +432,40 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
         float2 ls2[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) ls2[q] = make_float2(0.f, 0.f);
-        // Three of eight pairs on the FMA pipe: the exponentials of two streams
+        // Two of eight pairs on the FMA pipe: the exponentials of two streams
         // would keep the special-function units as long as the products keep the
-        // tensor cores. Not in masked blocks (its smallest value is not 0).
+        // tensor cores (packed batch: none so 115.6 us, one 112.9, two 112.5, three
+        // 113.3, four 113.9). Not in masked blocks (its smallest value is not 0), where 32 keys
+        // that no row of the warp sees are left out.
         auto weights = [&](auto plain) {
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
+          for (int c2 = 0; c2 < 2; ++c2) {
             uint32_t w[16];
+            if (plain.value || kh + c2 * 32 < warp_lim) {
+              uint32_t v[32];
+              seq::tmem_ld32(sa + c2 * 32, v);
+              tmem_ld_wait();
+              if (!plain.value) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 y = __ffma2_rn(make_float2(x[c4 * 32 + 2 * k], x[c4 * 32 + 2 * k + 1]), sl2, nm2);
-              const float2 p = plain.value && (kFma >> (k & 7) & 1)
-                                   ? seq::ex2_fma(y)
-                                   : make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
-              ls2[k & 3] = __fadd2_rn(ls2[k & 3], p);
-              w[k] = seq::pack_bf16(p.x, p.y);
+                for (int k = 0; k < 32; ++k)
+                  if (c2 * 32 + k >= n) v[k] = 0xff800000u;
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl2, nm2);
+                const float2 p = plain.value && (kFma >> (k & 7) & 1)
+                                     ? seq::ex2_fma(y)
+                                     : make_float2(seq::ex2_approx(y.x), seq::ex2_approx(y.y));
+                ls2[k & 3] = __fadd2_rn(ls2[k & 3], p);
+                w[k] = seq::pack_bf16(p.x, p.y);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = 0u;
             }
-            tmem_st16(sa + c4 * 16, w);
-            if (c4 == 1) {
-              // The first half of the keys: their product may start.
+            tmem_st16(sa + c2 * 16, w);
+            if (c2 == 0) {
+              // The first 32 keys of this half: their product may start.
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
@@ -448,7 +488,13 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
     }
     // ---------------- epilogue
     const bool have = my_nb > 0;
-    if (ok && (!have || warp_wait(&pvdone[s], (my_nb - 1) & 1))) {
+    if (ok && have && !warp_wait(&pvdone[s], (my_nb - 1) & 1)) fail();
+    if (ok && have && any_live) {
+      *mine = l_run;
+      ok = meet();
+      l_run = half ? *other + l_run : l_run + *other;
+    }
+    if (ok) {
       tc_fence_after();
       const bool seen = l_run > 0.f;
       const float inv = seen ? 1.f / l_run : 0.f;
@@ -457,40 +503,40 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
       const long long row = tok_g * a.Hkv * a.G + head;
       if (kSplit) {
         const long long at = (long long)z * rows + row;
-        if (live) a.part_l[at] = seen ? m_run + log2f(l_run) : -INFINITY;
-        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D);
+        if (live && half == 0) a.part_l[at] = seen ? m_run + log2f(l_run) : -INFINITY;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + half * (D / 2));
         if (any_live && have) {
 #pragma unroll
-          for (int c4 = 0; c4 < D / 32; ++c4) {
+          for (int c2 = 0; c2 < D / 64; ++c2) {
             uint32_t v[32];
-            seq::tmem_ld32(oa + c4 * 32, v);
+            seq::tmem_ld32(oa + c2 * 32, v);
             tmem_ld_wait();
             if (live) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                dst[c4 * 8 + k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                dst[c2 * 8 + k] = make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
                                               __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
             }
           }
         }
       } else {
-        if (live && a.lse) a.lse[row] = seen ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
-        uint32_t w[D / 2];
+        if (live && a.lse && half == 0) a.lse[row] = seen ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+        uint32_t w[D / 4];
 #pragma unroll
-        for (int c4 = 0; c4 < D / 32; ++c4) {
+        for (int c2 = 0; c2 < D / 64; ++c2) {
           uint32_t v[32];
-          seq::tmem_ld32(oa + c4 * 32, v);
+          seq::tmem_ld32(oa + c2 * 32, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            w[c4 * 16 + k] =
+            w[c2 * 16 + k] =
                 seen ? seq::pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv) : 0u;
         }
         // Through the stream's own Q tile, which its products have read. (Where it has
         // none, the tile's copy must have landed.)
         if (!have && nb_all > 0) warp_wait(qfull, 0);
-        seq::store_rows<D>(sQ + s * C::kTileBytes + quad * (32 * D * 2), w,
-                           live ? a.O + tok_g * a.o_row + (long long)head * D : nullptr);
+        seq::store_rows<D / 2>(sQ + s * C::kTileBytes + (half * 4 + quad) * (32 * D), w,
+                               live ? a.O + tok_g * a.o_row + (long long)head * D + half * (D / 2) : nullptr);
       }
     }
   }
@@ -568,10 +614,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
 //  - d = 64, and short sequences at d = 128: one stream a CTA, two CTAs to an SM: one's
 //    start and end hide behind the other's blocks.
 //  - Else two streams a CTA, which halves the reads of K and V.
-// Measured at d = 128, 24 / 8 heads, one stream (two): 16 x 256 tokens 34.8 (40.1) us,
-// 16 x 512 77.5 (83.1), 8 x 1024 97.8 (99.7), 8 x 1536 173 (170), 4 x 3000 264 (243),
-// 2 x 4096 229 (207); at d = 64, 8 / 8 heads: 16 x 512 23.7 (26.4), 8 x 1536 54.9
-// (59.8), 2 x 4096 64.9 (66.3).
+// Measured at d = 128, 24 / 8 heads, one stream (two): 16 x 256 tokens 33.1 (41.9) us,
+// 16 x 512 73.4 (86.0), 8 x 1024 92.5 (100), 8 x 1536 164 (172), 6 x 2048 195 (203),
+// 4 x 3000 253 (243), 2 x 4096 221 (206); at d = 64, 8 / 8 heads: 16 x 512 24.4 (26.7), 8 x 1536 55.9
+// (60.5), 2 x 4096 66.1 (67.0).
 struct Plan {
   int streams;
   bool split;

@@ -121,9 +121,9 @@ cudaError_t launch_behind(void (*fn)(P...), dim3 grid, unsigned threads, size_t 
 __device__ __forceinline__ void set_up(bool first) {
   if (first) {
     __syncwarp();
-    asm volatile("bar.arrive 7, %0;" ::"r"(blockDim.x) : "memory");
+    asm volatile("bar.arrive 15, %0;" ::"r"(blockDim.x) : "memory");
   } else {
-    asm volatile("bar.sync 7, %0;" ::"r"(blockDim.x) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
   }
 }
 
