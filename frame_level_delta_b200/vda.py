@@ -7,6 +7,7 @@ library has not been built; there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import numbers
 import os
 from typing import Dict, Optional, Tuple
 
@@ -627,6 +628,14 @@ def _signature(*tensors) -> tuple:
         return ()  # something that is no tensor: checked, and refused, every time
 
 
+def _number(scale):
+    """A call's scale is a plain number: a tensor's value may change while it stays the
+    same object, and reading it would synchronise."""
+    if scale is not None and type(scale) is not float and not isinstance(scale, numbers.Real):
+        raise ValueError(f"scale: expected a number, got {type(scale).__name__}")
+    return scale
+
+
 def _remember(key: tuple, value: tuple) -> tuple:
     if len(_checked) >= 4096:
         _checked.clear()
@@ -700,7 +709,7 @@ def causal_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: to
     of generation. ``scale`` defaults to 1 / sqrt(d). Returns O, or (O, lse) with
     lse [Tq, Hq] float32."""
     key = _signature(Q, K, V, cu_q, cu_k, k_len, O)
-    key = key and ("attention", key, scale)
+    key = key and ("attention", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(key, _check_attention(Q, K, V, cu_q, cu_k, k_len, scale, O))
     lse = None
 
@@ -743,7 +752,7 @@ def causal_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
     not written: uninitialised in tensors made here, as they were in ``out``."""
     given = None if out is None else (out.get("dQ"), out.get("dK"), out.get("dV"))
     key = _signature(Q, K, V, O, dO, lse, cu_q, cu_k, k_len, *(given or ()))
-    key = key and ("attention backward", key, scale)
+    key = key and ("attention backward", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(
         key, _check_attention_backward(Q, K, V, O, dO, lse, cu_q, cu_k, k_len, scale, given))
 
@@ -791,7 +800,7 @@ def decay_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay
     float32; S0 [N, H, d, d] float32, zero if not given. Returns O and the states
     after each sequence (``S`` may be S0: updated in place)."""
     key = _signature(Q, K, V, log_decay, cu, S0, O, S)
-    key = key and ("decay", key, scale)
+    key = key and ("decay", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(key, _check_decay(Q, K, V, log_decay, cu, S0, scale, O, S))
 
     def make():
@@ -825,7 +834,7 @@ def decay_attention_step(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_
     (vda_decay_attention_step): row n of Q, K, V [N, H, d] belongs to state S[n],
     which is updated in place. Returns O [N, H, d]."""
     key = _signature(Q, K, V, log_decay, S, O)
-    key = key and ("decay step", key, scale)
+    key = key and ("decay step", key, _number(scale))
     c, dev = _checked.get(key) or _remember(key, _check_decay_step(Q, K, V, log_decay, S, scale, O))
 
     def make():
@@ -869,7 +878,7 @@ def decay_attention_backward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, 
     not written: uninitialised in tensors made here, as they were in ``out``."""
     given = None if out is None else (out.get("dQ"), out.get("dK"), out.get("dV"), out.get("dS0"))
     key = _signature(Q, K, V, dO, log_decay, cu, S0, dS, *(given or ()))
-    key = key and ("decay backward", key, scale)
+    key = key and ("decay backward", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(
         key, _check_decay_backward(Q, K, V, dO, log_decay, cu, S0, dS, scale, given))
 

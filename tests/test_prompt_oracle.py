@@ -244,3 +244,24 @@ def test_binding_checks_rows():
             V._starts("cu", cu, cpu)
     with pytest.raises(ValueError, match="dtype"):
         V._starts("cu", torch.tensor([0, 3]), cpu)
+
+
+@pytest.mark.parametrize("scale", [torch.tensor(0.5), torch.ones(1), np.ones(()), "1"])
+def test_binding_takes_numbers_as_scale(scale):
+    """A call's checks are remembered by its scale: an object whose value can change is refused."""
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cu, g, lse, S = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(2), torch.zeros(4, 2), torch.zeros(4, 2, 64, 64)
+    for call in (lambda: V.causal_attention(q, q, q, cu, scale=scale),
+                 lambda: V.causal_attention_backward(q, q, q, q, q, lse, cu, scale=scale),
+                 lambda: V.decay_attention(q, q, q, g, cu, scale=scale),
+                 lambda: V.decay_attention_step(q, q, q, g, S, scale=scale),
+                 lambda: V.decay_attention_backward(q, q, q, q, g, cu, scale=scale)):
+        with pytest.raises(ValueError, match="scale"):
+            call()
+
+
+def test_binding_takes_any_real_scale():
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    for scale in (None, 1, 0.5, np.float32(0.5), np.float64(2.0)):
+        with pytest.raises(ValueError, match="CUDA devices"):
+            V.causal_attention(q, q, q, torch.tensor([0, 4], dtype=torch.int32), scale=scale)
