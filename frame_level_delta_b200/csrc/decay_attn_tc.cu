@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         seq::zero_row(tile_of(c, 2), C::kAtoms, row, kC);
       }
       fence_proxy_async_smem();
+      __syncwarp();
       asm volatile("bar.sync %0, 128;" ::"r"(1 + maker) : "memory");
     }
     if (g >= kMakers && !warp_wait(&vpempty[maker], g / kMakers - 1)) return false;
@@ -389,6 +390,17 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     __syncwarp();
     if (lane == 0) mbar_arrive(&vpfull[maker]);
     return true;
+  };
+  // A warp's steps, every kMakers-th. One whose wait gave up arrives at the group's
+  // barrier (a ragged chunk is the walk's last or first, so a group meets there once),
+  // so that the other three do not wait for it.
+  auto make_steps = [&](int maker, int steps) {
+    for (int g = maker; g < steps; g += kMakers)
+      if (!make_step(maker, g)) {
+        __syncwarp();
+        asm volatile("bar.arrive %0, 128;" ::"r"(1 + maker) : "memory");
+        break;
+      }
   };
 
   // 896 threads start with 72 registers each; the loading, issuing and V' warps give
@@ -621,9 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         if (lane == 0) mbar_arrive(ofull);
       }
     } else {
-      const int maker = (warp - 4) / 4;
-      for (int g = maker; g < nch * C::kSteps; g += kMakers)
-        if (!make_step(maker, g)) break;
+      make_steps((warp - 4) / 4, nch * C::kSteps);
     }
   } else if (warp < 20) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
@@ -729,9 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ---------------- V'
-    const int maker = kMakers - 2 + (warp - 20) / 4;
-    for (int g = maker; g < nch * C::kSteps; g += kMakers)
-      if (!make_step(maker, g)) break;
+    make_steps(kMakers - 2 + (warp - 20) / 4, nch * C::kSteps);
   }
 
   // ---------------- teardown
