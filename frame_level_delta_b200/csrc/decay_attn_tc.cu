@@ -23,8 +23,9 @@
 // in TMEM; O = Q X^T + (P / f_i) V, one accumulator, times f_i = a^(i+1) on the way
 // out, with X rounded to bf16 in shared memory (outputs are bf16, so each of the
 // two operand roundings adds what the output's own rounding is). f_i is held at
-// 2^-100 from below, so that P / f_i stays in range: where a head forgets faster,
-// 2^-100 of X, nothing next to the token's own term, stands for less.
+// 2^-64 from below, so that P / f_i stays in range (for outputs up to 2^63: held at
+// 2^-100, rows past a fast head's 69th overflowed from 2^27 on): where a head forgets
+// faster, 2^-64 of X, nothing next to the token's own term, stands for less.
 // W = V'^T K, where V' = a^(n-1-j) v_j enters
 // as three bf16 parts (24 bits together), so that the state, which is fp32
 // outside, keeps fp32 accuracy. W starts from zero in every chunk and is added to
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         int tok, n;
         chunk(c, tok, n);
         // log2 of 1 / f_i; f_i is a^(i+1) forward, a^(distance from the end) backward.
-        const float e_inv = fminf(-g2 * (float)(rev ? max(0, n - 1 - i) : i + 1), 100.f);
+        const float e_inv = fminf(-g2 * (float)(rev ? max(0, n - 1 - i) : i + 1), 64.f);
         const float inv = exp2f(e_inv);
         if (!(ok = warp_wait(sfull, c))) break;
         tc_fence_after();
