@@ -23,7 +23,11 @@
 //   buffers, dP = dO V_i^T, dS as bf16 over S, dQ += dS K_i.
 //
 // P and dS are rounded to bf16 for the products (the operand type); everything
-// else is fp32. Masked pairs are selected to zero, and rows that lie behind a
+// else is fp32. In blocks on the diagonal dS enters as two bf16 parts (16 bits
+// together): rows that see few keys, whose gradients are the largest, have all of
+// theirs there, and it is one product more for one block of a long row. (dQ and dK
+// against 64 bits: 2.6e-3 to 2.3e-3 of the norm, of which the results' own
+// rounding is 1.7e-3.) Masked pairs are selected to zero, and rows that lie behind a
 // sequence are zeroed in shared memory where a product sums over them.
 #include <cuda_bf16.h>
 
@@ -180,8 +184,9 @@ struct CbBars {
 
 // ---------------------------------------------------------------- dK and dV
 // TMEM: S^T | dP^T | dV | dK. Query column c of P^T (dS^T) lies, packed, at
-// column (c % 32) / 2 + (c / 32) * 32 of S^T (dP^T): each quarter of the
-// elementwise warps overwrites only columns that it has read itself.
+// column (c % 32) / 2 + (c / 32) * 32 of S^T (dP^T), dS^T's second part 16 columns
+// on: each quarter of the elementwise warps overwrites only columns that it has
+// read itself.
 template <int D>
 __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorMap* mK, const CUtensorMap* mV,
                                           const CUtensorMap* mG, const CbArgs& a, int bid, uint8_t* smem) {
@@ -235,6 +240,8 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
   const int i0 = min(tiles, max(0, k0 - shift) / a.tpt);
   const int n_it = tiles - i0;
   const int rows = a.tpt * a.G;
+  // Some row of the i-th tile does not see the whole key block.
+  auto on_diagonal = [&](int i) { return shift + (i0 + i) * a.tpt < k0 + kTile - 1; };
 
   // Rows that no tile has (128 is not a multiple of G) are summed over too: zero.
   for (int r = rows + (int)threadIdx.x; r < kTile; r += kThreads)
@@ -327,6 +334,11 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
         for (int kk = 0; kk < kTile / 16; ++kk)
           mma_f16_ts(tmem + (u ? kDK : kDV), tmem + (u ? kDP : kS) + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128,
                      C::kIdescG, (i > 0 || kk > 0) ? 1u : 0u);
+        if (u && on_diagonal(i)) {  // the second parts
+#pragma unroll 1
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_f16_ts(tmem + kDK, tmem + kDP + 16 + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128, C::kIdescG, 1u);
+        }
         return true;
       };
       ok = ok && issue_sd(0, 0) && issue_sd(0, 1);
@@ -356,7 +368,7 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
       const bool ragged = t0 + a.tpt > nq;
       // Every key of the block is seen by every row of the tile. (Where 128 is not a
       // multiple of G, the columns that are no rows are zero in Q and dO.)
-      const bool full = !ragged && shift + t0 >= k0 + kTile - 1;
+      const bool diagonal = on_diagonal(i), full = !ragged && !diagonal;
       // Else this row's key is seen by columns first .. end - 1 (token >= key - shift).
       const int first = max(0, (key - shift - t0)) * a.G - part * 32;
       const int end = min(a.tpt, nq - t0) * a.G - part * 32;
@@ -414,11 +426,21 @@ __device__ __forceinline__ void attn_dkdv(const CUtensorMap* mQ, const CUtensorM
         const float2 y = __fmul2_rn(p[k + 1], __fadd2_rn(make_float2(__uint_as_float(v[2 * k + 2]),
                                                                      __uint_as_float(v[2 * k + 3])),
                                                          make_float2(l.z, l.w)));
+        if (diagonal) {
+          p[k] = x;
+          p[k + 1] = y;
+        }
         w[k] = seq::pack_bf16(x.x, x.y);
         w[k + 1] = seq::pack_bf16(y.x, y.y);
       }
       if (!full) mask(w);
       tmem_st16(da, w);
+      if (diagonal) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = seq::pack_rest(p[k], w[k]);
+        mask(w);
+        tmem_st16(da + 16, w);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -514,6 +536,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
   const int shift = nk - nq;
   const int last = min(t0 + a.tpt, nq) - 1;
   const int n_it = (min(nk, max(0, shift + last + 1)) + kTile - 1) / kTile;
+  const int min_lim = shift + t0 + 1;  // keys the tile's first row sees
   const int rows = a.tpt * a.G;
 
   seq::set_up(warp == 0);
@@ -588,6 +611,12 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
         for (int kk = 0; kk < kTile / 16; ++kk)
           mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128, C::kIdescG,
                      (i > 0 || kk > 0) ? 1u : 0u);
+        if ((i + 1) * kTile > min_lim) {  // on the diagonal: the second parts
+#pragma unroll 1
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_f16_ts(tmem + kDQ, tmem + kS + (i & 1) * 128 + 16 + (kk / 2) * 32 + (kk % 2) * 8, db + kk * 128,
+                       C::kIdescG, 1u);
+        }
         mma_commit(&b.rempty[slot]);
       }
       if (ok) mma_commit(b.done);
@@ -602,7 +631,6 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
     const int tok = t0 + r / a.G;
     const bool live = r < rows && tok < nq;
     const int lim = min(nk, shift + tok + 1);
-    const int min_lim = shift + t0 + 1;
     const float2 st = live ? a.stat[((long long)hk * a.Tq + q_lo + t0) * a.G + r] : make_float2(0.f, 0.f);
     const float2 sl2 = make_float2(a.sl, a.sl), nl2 = make_float2(-st.x, -st.x), nd2 = make_float2(-st.y, -st.y);
     bool ok = true;
@@ -628,13 +656,19 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap* mQ, const CUtensorMap
       for (int k = 0; k < 16; ++k) {
         const float2 x = __fmul2_rn(
             p[k], __fadd2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), nd2));
+        p[k] = x;
         w[k] = seq::pack_bf16(x.x, x.y);
       }
       if (k0 + kTile > min_lim) {
         const int end = lim - k0 - part * 32;
+        uint32_t rest[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          w[k] = (2 * k < end ? w[k] & 0xffffu : 0u) | (2 * k + 1 < end ? w[k] & 0xffff0000u : 0u);
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t seen = (2 * k < end ? 0xffffu : 0u) | (2 * k + 1 < end ? 0xffff0000u : 0u);
+          rest[k] = seq::pack_rest(p[k], w[k]) & seen;
+          w[k] &= seen;
+        }
+        tmem_st16(sa + 16, rest);
       }
       tmem_st16(sa, w);
       tmem_st_wait();

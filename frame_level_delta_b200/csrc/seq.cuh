@@ -197,6 +197,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return sm100::bf162_bits(__floats2bfloat162_rn(a, b));
 }
 
+// What a pair's packed bf16 values leave of it, packed.
+__device__ __forceinline__ uint32_t pack_rest(float2 x, uint32_t w) {
+  return pack_bf16(x.x - __uint_as_float(w << 16), x.y - __uint_as_float(w & 0xffff0000u));
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
