@@ -78,7 +78,8 @@ struct DaCfg {
   static constexpr int kXOff = 6 * kTileBytes;
   static constexpr int kBarOff = kXOff + D * D * 2;
   static constexpr int kSmemBytes = kBarOff + 2048 + 1024;
-  // TMEM columns: S1, O, W; V' in 64 columns a buffer (three parts of 16).
+  // TMEM columns: S1, O, W (where there is room two of D columns, see kWs); V' in 64
+  // columns a buffer (three parts of 16).
   static constexpr uint32_t kS1 = 0, kO = 128, kW = 256, kVp = 384;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescS = sm100::idesc_bf16_f32(128, 128, false, false);
@@ -195,6 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   // step. Where no output is made all four groups do, in the columns S1 and O leave.
   constexpr int kMakers = kStateOnly ? 4 : 2;
   constexpr uint32_t kVpCol = kStateOnly ? 0 : C::kVp;
+  // Buffers of W: with two the next chunk's products need not wait until the state's
+  // warps have read the last one's. Only with outputs at d = 128 all columns are taken.
+  constexpr int kWs = kStateOnly || D == 64 ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* sX = smem + C::kXOff;
@@ -207,9 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   uint64_t* oempty = odone + 1;
   uint64_t* vpfull = oempty + 1;  // [kMakers]
   uint64_t* vpempty = vpfull + kMakers;
-  uint64_t* wfull = vpempty + kMakers;
-  uint64_t* wempty = wfull + 1;
-  uint64_t* xfull = wempty + 1;
+  uint64_t* wfull = vpempty + kMakers;  // [kWs]
+  uint64_t* wempty = wfull + kWs;
+  uint64_t* xfull = wempty + kWs;
   uint64_t* ofull = xfull + 1;  // an output tile is staged
   uint64_t* drain = ofull + 1;  // both issuing warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
   int* scratch = reinterpret_cast<int*>(tmem_slot + 4);
   float* pw = reinterpret_cast<float*>(scratch + 40);  // [32 + 64], see below
   float* wt = pw + 96;                                 // [256] weights of V' in a whole chunk, then zeros
-  static_assert((23 + 2 * kMakers) * 8 + 16 + 160 + 4 * (96 + 256) + 16 <= 2048, "barrier block overflows its allowance");
+  static_assert((21 + 2 * kMakers + 2 * kWs) * 8 + 16 + 160 + 4 * (96 + 256) + 16 <= 2048, "barrier block overflows its allowance");
 
   if (kStateOnly) seq::grid_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -247,8 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       mbar_init(&vpfull[i], 4);
       mbar_init(&vpempty[i], 1);
     }
-    mbar_init(wfull, 1);
-    mbar_init(wempty, 8);
+    for (int i = 0; i < kWs; ++i) {
+      mbar_init(&wfull[i], 1);
+      mbar_init(&wempty[i], 8);
+    }
     mbar_init(xfull, 8);
     mbar_init(ofull, 8);
     mbar_init(drain, 2);
@@ -479,25 +485,27 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
           const uint64_t dk = smem_desc_sw128(smem_u32(tile_of(c, 1)), kC * 128, 1024);
+          const int wb = c % kWs;
+          const uint32_t w_at = tmem + C::kW + wb * D;
           if (!(ok = wait1(&rfull[slot_of(c, 1)], c / kStages))) break;
 #pragma unroll 1
           for (int q = 0; q < C::kSteps; ++q) {
             const int g = c * C::kSteps + q, maker = g % kMakers;
             if (!(ok = wait1(&vpfull[maker], g / kMakers))) break;
-            if (q == 0 && c > 0 && !(ok = wait1(wempty, c - 1))) break;
+            if (q == 0 && c >= kWs && !(ok = wait1(&wempty[wb], c / kWs - 1))) break;
             tc_fence_after();
             const uint32_t av = tmem + kVpCol + maker * 64;
 #pragma unroll 1
             for (int p3 = 0; p3 < 3; ++p3)
 #pragma unroll
               for (int kk = 0; kk < C::kStep / 16; ++kk)
-                mma_f16_ts(tmem + C::kW, av + p3 * 16 + kk * 8, dk + (q * (C::kStep / 16) + kk) * 128, C::kIdescPV,
+                mma_f16_ts(w_at, av + p3 * 16 + kk * 8, dk + (q * (C::kStep / 16) + kk) * 128, C::kIdescPV,
                            (q > 0 || p3 > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&vpempty[maker]);
           }
           if (!ok) break;
           smem_release_u32(v_read, c + 1);
-          mma_commit(wfull);
+          mma_commit(&wfull[wb]);
           mma_commit(&rempty[slot_of(c, 1)]);
           mma_commit(&rempty[slot_of(c, 2)]);
           if (kStateOnly) {
@@ -654,6 +662,34 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
         if (tr) {
 #pragma unroll
           for (int k = 0; k < kCols; ++k) X[k] = src[(half * kCols + k) * D + row];
+        } else if constexpr (D == 128) {
+          // Whole lines of the warp's 32 rows, then by way of shared memory (32 columns at
+          // a time, in the part of the operand that this warp writes) to the rows' threads:
+          // from those threads the loads took 4.5 us.
+          uint8_t* st = sX + half * (D * 128) + quad * 4096;
+          const float* at = src + (quad * 32 + lane / 8) * D + half * kCols + lane % 8 * 4;
+          float4 in[2][8];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) in[u / 8][u % 8] = *reinterpret_cast<const float4*>(at + u % 8 * 4 * D + u / 8 * 32);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + lane / 8;
+              *reinterpret_cast<float4*>(st + r * 128 + ((lane ^ r) & 7) * 16) = in[u][i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 x = *reinterpret_cast<const float4*>(st + lane * 128 + ((lane ^ k) & 7) * 16);
+              float* to = &X[u * 32 + k * 4];
+              to[0] = x.x;
+              to[1] = x.y;
+              to[2] = x.z;
+              to[3] = x.w;
+            }
+            __syncwarp();
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
@@ -686,13 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     auto take_w = [&](int c) -> bool {
       int tok, n;
       chunk(c, tok, n);
-      if (!warp_wait(wfull, c)) return false;
+      const int wb = c % kWs;
+      if (!warp_wait(&wfull[wb], c / kWs)) return false;
       tc_fence_after();
       const float f = power(g2, n);
 #pragma unroll
       for (int k4 = 0; k4 < kCols / 16; ++k4) {
         uint32_t v[16];
-        tmem_ld16(tmem + lane_off + C::kW + half * kCols + k4 * 16, v);
+        tmem_ld16(tmem + lane_off + C::kW + wb * D + half * kCols + k4 * 16, v);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -705,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(wempty);
+      if (lane == 0) mbar_arrive(&wempty[wb]);
       return true;
     };
     bool ok = true;
@@ -761,7 +798,6 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   constexpr int kBatch = 8;
   __shared__ int scratch;
   seq::grid_trigger();
-  seq::grid_wait();
   const int sq = blockIdx.y;
   const int jb = blockIdx.x % a.njobs, h = (blockIdx.x / a.njobs) % a.H;
   const int slice = blockIdx.x / a.njobs / a.H;
@@ -771,10 +807,16 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   seq::bounds(a.cu, sq, a.T, lo, hi);
   const int len = hi - lo;
   const int nparts = max(1, (len + seg_tokens - 1) / seg_tokens);
-  if (nparts == 1) return;
+  if (nparts == 1) {
+    seq::grid_wait();
+    return;
+  }
   const int first_s = segments_before(a, sq, &scratch);
   // Sequences that overlap (a wrong prefix array) have more segments than there is room for.
-  if (first_s + nparts > a.items) return;
+  if (first_s + nparts > a.items) {
+    seq::grid_wait();
+    return;
+  }
   const int e = (slice * 256 + threadIdx.x) * 4;
   const int r = e / D, c = e % D;
   const float g2 = head_decay(a, h);
@@ -788,6 +830,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   }
   const int nch = (len + kC - 1) / kC;
   const long long stride = (long long)a.H * a.njobs * (D * D);
+  seq::grid_wait();  // all that is read before is the caller's
   float* base = a.seg_state + (((long long)first_s * a.H + h) * a.njobs + jb) * (D * D) + e;
   for (int p0 = 0; p0 < nparts; p0 += kBatch) {  // the loads of a batch are in flight together
     float4 y[kBatch];
