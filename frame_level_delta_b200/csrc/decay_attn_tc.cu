@@ -291,8 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
     const int at = segments_before(a, sq, scratch) + part;
     if (at < a.items) seg_state = a.seg_state + (((long long)at * a.H + h) * a.njobs + jb) * (D * D);
   }
-  // First token (within the tensor) and token count of processing-order chunk c.
+  // First token (within the tensor) and token count of the c-th chunk in processing order.
+  // A segment's own state is formed from its last chunk to its first, so that what the
+  // main launch reads first is what L2 has seen last.
   auto chunk = [&](int c, int& tok, int& n) {
+    if (kStateOnly) c = nch - 1 - c;
     const int cc = rev ? nch_all - 1 - (p0 + c) : p0 + c;
     tok = lo + cc * kC;
     n = min(kC, len - cc * kC);
@@ -718,14 +721,16 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(xfull);
     };
-    // X' = a^n X + W of chunk c.
+    // X' = a^n X + W of chunk c; from the last chunk to the first X' = X + a^(tokens behind) W.
+    int seg_lo = 0, seg_hi = 0;
+    if (kStateOnly) chunk_tokens(len, rev, p0, p0 + nch, seg_lo, seg_hi);
     auto take_w = [&](int c) -> bool {
       int tok, n;
       chunk(c, tok, n);
       const int wb = c % kWs;
       if (!warp_wait(&wfull[wb], c / kWs)) return false;
       tc_fence_after();
-      const float f = power(g2, n);
+      const float f = power(g2, !kStateOnly ? n : rev ? tok - lo - seg_lo : seg_hi - (tok - lo + n));
 #pragma unroll
       for (int k4 = 0; k4 < kCols / 16; ++k4) {
         uint32_t v[16];
@@ -734,8 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_attn_tc_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
           float* x = &X[k4 * 16 + k];
-          const float2 y = __ffma2_rn(make_float2(f, f), make_float2(x[0], x[1]),
-                                      make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+          const float2 w = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          const float2 was = make_float2(x[0], x[1]);
+          const float2 y = __ffma2_rn(make_float2(f, f), kStateOnly ? w : was, kStateOnly ? was : w);
           x[0] = y.x;
           x[1] = y.y;
         }
