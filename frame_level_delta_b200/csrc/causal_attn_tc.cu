@@ -50,19 +50,26 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kMinSplitBlocks = 4;
-constexpr int kSplitCtas = 8;  // CTAs per SM that the split form aims at
+constexpr int kFewRows = 32;  // 48 ragged caches: 133 us with whole tiles, 129 so
+// CTAs per SM that the split form aims at. Measured with 48 ragged caches of up to 8192 slots,
+// 32 / 8 heads (16; 32 of them): two 163 (76; 114) us, three 139 (73; 115), four 138 (74; 120),
+// five 138 (80; 120), eight 146 (83; 125).
+constexpr int kSplitCtas = 4;
 constexpr int kShortKeys = 2304;  // d = 128: mean keys below which a CTA has one stream
 constexpr uint32_t kFma = 0x22;  // pairs of eight whose exponentials the FMA pipe takes
 
-template <int D, int kStreams>
+template <int D, int kStreams, bool kFew>
 struct CaCfg {
   static constexpr int kThreads = 128 + 256 * kStreams;  // TMA warp, MMA warp, two idle ones, eight warps a stream
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
   // Key and value blocks in flight, one ring.
-  static constexpr int kRing = kStreams == 2 || D == 64 ? 5 : 2;
+  static constexpr int kRing = kFew ? (D == 64 ? 6 : 3) : kStreams == 2 || D == 64 ? 5 : 2;
+  // A tile of few rows keeps kFewRows of Q only: the products take whatever lies behind
+  // them for the other rows, which are none.
+  static constexpr int kQAtom = (kFew ? kFewRows : kTile) * 128, kQBytes = kAtoms * kQAtom;
   static constexpr int kQOff = 0;
-  static constexpr int kRingOff = kStreams * kTileBytes;
+  static constexpr int kRingOff = kStreams * kQBytes;
   static constexpr int kBarOff = kRingOff + kRing * kTileBytes;
   static constexpr int kPairOff = kBarOff + 512;  // per stream, half and row: what a row's two threads exchange
   static constexpr int kSmemBytes = kPairOff + kStreams * 1024;  // the array is declared 1024-byte aligned
@@ -105,11 +112,11 @@ __device__ __forceinline__ int used_splits(int nb, int nsplit) {
   return max(1, min(nsplit, (nb + kMinSplitBlocks - 1) / kMinSplitBlocks));
 }
 
-template <int D, int kStreams, bool kSplit>
-__global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
+template <int D, int kStreams, bool kSplit, bool kFew>
+__global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStreams)
     causal_attn_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                           const __grid_constant__ CUtensorMap mV, const CaArgs a) {
-  using C = CaCfg<D, kStreams>;
+  using C = CaCfg<D, kStreams, kFew>;
   using namespace sm100;
   extern __shared__ __align__(1024) uint8_t smem_1024[];
   uint8_t* smem = smem_1024;
@@ -157,15 +164,23 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
   const int rest = blockIdx.x / a.Hkv;
   const int z = kSplit ? rest % a.nsplit : 0;
   const int per_item = kStreams * a.tpt;
-  int idx;
-  const int sq = seq::find_item(
-      kSplit ? rest / a.nsplit : rest, a.N, scratch, reinterpret_cast<int*>(sQ),
-      [&](int i) {
-        int lo, hi;
-        seq::bounds(a.cu_q, i, a.Tq, lo, hi);
-        return hi - lo;
-      },
-      [&](int n) { return (n + per_item - 1) / per_item; }, idx);
+  int idx, sq;
+  auto tokens = [&](int i) {
+    int lo, hi;
+    seq::bounds(a.cu_q, i, a.Tq, lo, hi);
+    return hi - lo;
+  };
+  auto tiles = [&](int n) { return (n + per_item - 1) / per_item; };
+  if constexpr (kSplit) {
+    // Few rows: a sequence's work goes by its keys.
+    sq = seq::find_item(rest / a.nsplit, a.N, scratch, reinterpret_cast<int*>(sQ), tokens, tiles, idx, [&](int i) {
+      int lo, n;
+      key_range(a, i, lo, n);
+      return n;
+    });
+  } else {
+    sq = seq::find_item(rest, a.N, scratch, reinterpret_cast<int*>(sQ), tokens, tiles, idx);
+  }
   auto leave = [&] {
     __syncthreads();
     tc_fence_after();
@@ -218,12 +233,12 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
       // warp takes blocks: K0, then V_t and the next K in turn.
       if (nb_all > 0 && seq::elect_one()) {
         const uint32_t q_bytes = (uint32_t)(a.tpt * a.G) * 128u;
-        const int tiles = nb[1] > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * tiles);
-        for (int s = 0; s < tiles; ++s)
+        const int q_tiles = nb[1] > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(qfull, q_bytes * C::kAtoms * q_tiles);
+        for (int s = 0; s < q_tiles; ++s)
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
-            tma_load_3d(sQ + s * C::kTileBytes + at * (kTile * 128), &mQ, qfull, at * 64, hk * a.G, q_lo + t0[s]);
+            tma_load_3d(sQ + s * C::kQBytes + at * C::kQAtom, &mQ, qfull, at * 64, hk * a.G, q_lo + t0[s]);
         int issued = 0;  // ring copies
         auto load = [&](const CUtensorMap* m, int blk) -> bool {
           const int slot = issued % C::kRing;
@@ -263,12 +278,13 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams>::kThreads), 3 - kStreams)
         };
         auto issue_s = [&](int s, int slot) {
           // The address field of a descriptor counts 16 bytes: steps are added to it.
-          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + s * C::kTileBytes), 16, 1024);
+          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + s * C::kQBytes), 16, 1024);
           const uint64_t dk = smem_desc_sw128(smem_u32(sR + slot * C::kTileBytes), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) / 16;
-            mma_f16(tmem + C::kS + s * 128, dq + off, dk + off, C::kIdescS, kk > 0 ? 1u : 0u);
+            const uint32_t q_off = ((kk / 4) * C::kQAtom + (kk % 4) * 32) / 16;
+            mma_f16(tmem + C::kS + s * 128, dq + q_off, dk + off, C::kIdescS, kk > 0 ? 1u : 0u);
           }
           mma_commit(&sfull[s]);
         };
@@ -610,7 +626,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
 // The form and the number of key shares for a call, by mean lengths (the lengths
 // themselves are on the device).
 //  - Few rows on long keys: one stream a CTA, the keys shared out, in enough shares
-//    to give each SM several CTAs.
+//    to give each SM several CTAs. Where a sequence has up to kFewRows rows on average,
+//    tiles are that high, which leaves room for one more block in flight.
 //  - d = 64, and short sequences at d = 128: one stream a CTA, two CTAs to an SM: one's
 //    start and end hide behind the other's blocks.
 //  - Else two streams a CTA, which halves the reads of K and V.
@@ -622,18 +639,20 @@ struct Plan {
   int streams;
   bool split;
   int nsplit;
+  int tpt;
 };
 Plan plan_of(const vda_attention_config& c) {
   const int G = c.Hq / c.Hkv, tpt = kTile / G;
-  const long long tiles = ((long long)c.Tq / tpt + c.N) * c.Hkv;
   const long long ctas = ((long long)c.Tq / (2 * tpt) + (c.N + 1) / 2) * c.Hkv;
   const long long keys = (long long)c.Tk / c.N;  // mean room per sequence
   const long long rows = (long long)c.Tq / c.N;
   const bool few = (long long)c.Tq <= (long long)c.N * tpt;  // about one tile per sequence
-  Plan p{few || c.d == 64 || keys < kShortKeys ? 1 : 2, false, 1};
+  Plan p{few || c.d == 64 || keys < kShortKeys ? 1 : 2, false, 1, tpt};
   if (keys >= 2 * kMinSplitBlocks * kTile && (few || (ctas < 148 && keys >= 4 * rows))) {
     p.streams = 1;
     p.split = true;
+    if (G <= kFewRows && c.Tq <= (long long)c.N * (kFewRows / G)) p.tpt = kFewRows / G;
+    const long long tiles = ((long long)c.Tq / p.tpt + c.N) * c.Hkv;
     const long long want = (148LL * kSplitCtas + tiles - 1) / tiles;
     const long long most = std::max(1LL, ((long long)c.Tk + kTile * kMinSplitBlocks - 1) / (kTile * kMinSplitBlocks));
     p.nsplit = (int)std::max(1LL, std::min({want, most, 64LL}));
@@ -645,10 +664,11 @@ template <int D>
 cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K, const void* V, const int* cu_q,
                      const int* cu_k, const int* k_len, void* O, float* lse, void* ws, uint32_t* status,
                      cudaStream_t s) {
-  using C1 = CaCfg<D, 1>;
+  using C1 = CaCfg<D, 1, false>;
+  using CF = CaCfg<D, 1, true>;
   const Plan p = plan_of(c);
   CaArgs a{};
-  a.N = c.N; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.tpt = kTile / a.G; a.Tq = c.Tq; a.Tk = c.Tk;
+  a.N = c.N; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv; a.tpt = p.tpt; a.Tq = c.Tq; a.Tk = c.Tk;
   a.nsplit = p.nsplit;
   a.cu_q = cu_q; a.cu_k = cu_k; a.k_len = k_len;
   a.sl = c.scale * 1.4426950408889634f;
@@ -667,12 +687,15 @@ cudaError_t launch_d(const vda_attention_config& c, const void* Q, const void* K
   const long long items = (long long)c.Tq / per_item + c.N;
   const long long grid = items * c.Hkv * p.nsplit;
   if (grid >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-  auto* fn = p.split ? causal_attn_tc_kernel<D, 1, true> : causal_attn_tc_kernel<D, 1, false>;
-  int threads = C1::kThreads, smem = C1::kSmemBytes;
+  const bool few = p.tpt < kTile / a.G;
+  auto* fn = few       ? causal_attn_tc_kernel<D, 1, true, true>
+             : p.split ? causal_attn_tc_kernel<D, 1, true, false>
+                       : causal_attn_tc_kernel<D, 1, false, false>;
+  int threads = C1::kThreads, smem = few ? CF::kSmemBytes : C1::kSmemBytes;
   if constexpr (D == 128) {
-    using C2 = CaCfg<D, 2>;
+    using C2 = CaCfg<D, 2, false>;
     if (p.streams == 2) {
-      fn = causal_attn_tc_kernel<D, 2, false>;
+      fn = causal_attn_tc_kernel<D, 2, false, false>;
       threads = C2::kThreads;
       smem = C2::kSmemBytes;
     }

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sm100.cuh"
 
 namespace vda {
@@ -21,7 +23,7 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int T, int& lo, int
 
 // Work item x of a list in which a sequence of size n has count(n) items (size(i):
 // sequence i's tokens): returns the sequence and x's index within it, or -1 past the
-// list's end. Up to kSorted sequences, the largest come first, so that no long one
+// list's end. Up to kSorted sequences, the largest (by key(i), or by size) come first, so that no long one
 // starts when the others are done; beyond, in their order. Every thread of the block
 // calls it; `scratch` holds 40 ints, `big` 2 kSorted. Up to 32 sequences each warp
 // finds the item by itself, so the warp that loads can start at once (a search by the
@@ -29,11 +31,19 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int T, int& lo, int
 // each pass takes blockDim.x sequences (one load and one scan). The caller
 // synchronises the block.
 constexpr int kSorted = 128;
-template <typename Size, typename Count>
-__device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, Size size, Count count, int& idx) {
+struct BySize {};
+template <typename Size, typename Count, typename Key = BySize>
+__device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, Size size, Count count, int& idx,
+                                         Key key = Key()) {
+  constexpr bool by_size = std::is_same<Key, BySize>::value;
+  auto key_of = [&](int i, int n) {
+    if constexpr (by_size) return n;
+    else return key(i);
+  };
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
   if (N <= 32) {
-    const int own = lane < N ? size(lane) : 0, c = lane < N ? count(own) : 0;
+    const int n_own = lane < N ? size(lane) : 0, c = lane < N ? count(n_own) : 0;
+    const int own = lane < N ? key_of(lane, n_own) : 0;
     int lo = 0;  // items of the sequences before this lane's
 #pragma unroll 4
     for (int j = 0; j < N; ++j) {
@@ -50,7 +60,7 @@ __device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, S
   const bool sorted = N <= kSorted;
   int own = 0;
   if (sorted) {
-    if (t < N) big[t] = own = size(t);
+    if (t < N) big[t] = own = key_of(t, by_size ? size(t) : 0);
     __syncthreads();
     if (t < N) {
       int rank = 0;
@@ -62,7 +72,7 @@ __device__ __forceinline__ int find_item(int x, int N, int* scratch, int* big, S
   for (int base = 0; base < N; base += blockDim.x) {
     const int i = base + t;
     const int sq = sorted && i < N ? big[kSorted + i] : i;
-    const int c = i < N ? count(sorted ? big[sq] : size(sq)) : 0;
+    const int c = i < N ? count(by_size && sorted ? big[sq] : size(sq)) : 0;
     int inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
