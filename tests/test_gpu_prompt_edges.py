@@ -71,3 +71,30 @@ def test_gradients_on_the_diagonal_are_rounded_once(Hq, Hkv, d):
     for n, w in want.items():
         once = np.linalg.norm(f64(torch.from_numpy(w).to(torch.bfloat16)) - w)
         assert np.linalg.norm(f64(got[n]) - w) <= 1.1 * once, n
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(6, 2, 128), (4, 4, 64), (32, 1, 128)])
+@pytest.mark.parametrize("N", [8, 40])
+def test_few_tokens_on_long_caches(Hq, Hkv, d, N):
+    """Some sequences with more tokens than a tile of few rows has, one without any, caches
+    that are empty or shorter than the new tokens, NaN in the room behind them."""
+    room = 1100
+    nq = ([1, 33, 1, 0, 2, 1, 1, 1] if Hq < 32 else [1, 2, 1, 0, 1, 1, 1, 1]) * (N // 8)
+    lens = ([1100, 129, 0, 700, 1, 1024, 1099, 513] * (N // 8))
+    T = sum(nq)
+    tail = 3 if Hq < 32 else 0  # (rows behind count for the choice of form)
+    Q, K, Vv = rand(81, T + tail, Hq, d, scale=1.5), rand(82, N * room, Hkv, d), rand(83, N * room, Hkv, d)
+    for i, n in enumerate(lens):
+        K[i * room + n:(i + 1) * room] = float("nan")
+        Vv[i * room + n:(i + 1) * room] = float("nan")
+    kr = [(i * room, i * room + n) for i, n in enumerate(lens)]
+    ref = po.causal_attention(f64(Q), f64(K), f64(Vv), ranges(nq), kr, d ** -0.5)
+    O = torch.full_like(Q, float("nan"), device=DEV)
+    _, lse = V.causal_attention(Q.to(DEV), K.to(DEV), Vv.to(DEV), starts(nq, DEV), cu_k=starts([room] * N, DEV),
+                                k_len=torch.tensor(lens, dtype=torch.int32, device=DEV), O=O, return_lse=True)
+    bounded(f64(O), ref["O"], ref["abs_O"], "O")
+    assert np.isnan(f64(O)[T:]).all()
+    w, g = ref["lse"][:T], f64(lse)[:T]
+    assert np.array_equal(np.isneginf(g), np.isneginf(w))
+    ok = np.isfinite(w)
+    assert np.abs(g[ok] - w[ok]).max() <= 2.0 ** -11 + 1e-6 * np.abs(w[ok]).max()
