@@ -386,6 +386,7 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
         if (!warp_wait(&rfull[slot], (pos / C::kRing) & 1)) { fail(); break; }
         if (k0 + r >= nk) seq::zero_row(sR + slot * C::kTileBytes, C::kAtoms, r, kTile);
         fence_proxy_async_smem();
+        __syncwarp();  // every lane's rows, before lane 0 signals the product that reads them
       }
       if (any_live) {
         const bool masked = k0 + kTile > min_lim;
