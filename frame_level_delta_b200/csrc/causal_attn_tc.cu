@@ -32,8 +32,10 @@
 //
 // Masks select: a masked logit becomes -inf whatever it was, and value rows past
 // a sequence's end are zeroed in shared memory before the product that reads
-// them, so neither infinities nor NaN behind a sequence reach a result. Within a
-// sequence, values are expected to be finite.
+// them, so neither infinities nor NaN behind a sequence reach a result. What is not
+// finite within a sequence is not hidden: a row that sees a logit of NaN or +inf (or
+// nothing but -inf) gives NaN, as the softmax's definition does. (A value that is not
+// finite also reaches the rows of its block that do not see it, as 0 x NaN.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -408,16 +410,19 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
 #pragma unroll
           for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(v[q]);
 #pragma unroll
-          for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
-          mb = fmaxf(mb, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          for (int k = 4; k < 32; ++k) mx[k & 3] = seq::max_nan(mx[k & 3], __uint_as_float(v[k]));
+          mb = seq::max_nan(mb, seq::max_nan(seq::max_nan(mx[0], mx[1]), seq::max_nan(mx[2], mx[3])));
         }
         mb *= a.sl;
         // (The other thread has read the last block's: the product that this block's
         // logits came behind waited for its probabilities.)
         *mine = mb;
         if (!meet()) { fail(); break; }
-        mb = fmaxf(mb, *other);
-        const bool grow = j > 0 && mb > m_run + 8.f;
+        mb = seq::max_nan(mb, *other);
+        // A NaN among a row's logits, or one beyond the range, makes its weights NaN, and
+        // so its O and its sum: the maximum carries it, and stays NaN from here on.
+        if (!(mb < INFINITY)) mb = NAN;
+        const bool grow = live && j > 0 && !(mb <= m_run + 8.f);
         if (j == 0) m_run = mb;
         if (__any_sync(0xffffffffu, grow)) {
           if (!warp_wait(&pvdone[s], (j - 1) & 1)) { fail(); break; }
@@ -513,14 +518,15 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
     }
     if (ok) {
       tc_fence_after();
-      const bool seen = l_run > 0.f;
-      const float inv = seen ? 1.f / l_run : 0.f;
+      // No finite logit: the row sees no key, or -inf - (-inf) of those it sees is NaN.
+      const bool none = m_run == -INFINITY, sees = lim > 0;
+      const float inv = none ? 0.f : 1.f / l_run;
       const long long tok_g = (long long)q_lo + (live ? tok : 0);
       const long long rows = (long long)a.Tq * a.Hkv * a.G;
       const long long row = tok_g * a.Hkv * a.G + head;
       if (kSplit) {
         const long long at = (long long)z * rows + row;
-        if (live && half == 0) a.part_l[at] = seen ? m_run + log2f(l_run) : -INFINITY;
+        if (live && half == 0) a.part_l[at] = none ? -INFINITY : m_run + log2f(l_run);
         float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + half * (D / 2));
         if (any_live && have) {
 #pragma unroll
@@ -537,7 +543,9 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
           }
         }
       } else {
-        if (live && a.lse && half == 0) a.lse[row] = seen ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+        if (live && a.lse && half == 0)
+          a.lse[row] = none ? (sees ? NAN : -INFINITY) : (m_run + log2f(l_run)) * 0.6931471805599453f;
+        const uint32_t fill = sees ? 0x7fff7fffu : 0u;  // two bf16 NaN
         uint32_t w[D / 4];
 #pragma unroll
         for (int c2 = 0; c2 < D / 64; ++c2) {
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             w[c2 * 16 + k] =
-                seen ? seq::pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv) : 0u;
+                none ? fill : seq::pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
         }
         // Through the stream's own Q tile, which its products have read. (Where it has
         // none, the tile's copy must have landed.)
@@ -598,17 +606,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
   const int n = used_splits(nb, a.nsplit);
   seq::grid_wait();
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_l[i * rows + row]);
+  for (int i = lane; i < n; i += 32) m = seq::max_nan(m, a.part_l[i * rows + row]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = seq::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   constexpr int kPer = D / 32;
   float acc[kPer], w_all = 0.f;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  if (m > -INFINITY) {
+  const bool none = m == -INFINITY;
+  if (!none) {
     for (int i = 0; i < n; ++i) {
       const float l = a.part_l[i * rows + row];
-      if (l == -INFINITY) continue;  // a share without visible keys has written no o
+      if (l == -INFINITY) continue;  // a share without a finite logit has no weight (without keys, it has written no o)
       const float w = exp2f(l - m);
       w_all += w;
       const float* src = a.part_o + (i * rows + row) * D + lane * kPer;
@@ -616,12 +625,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
       for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, src[k], acc[k]);
     }
   }
-  const float inv = w_all > 0.f ? 1.f / w_all : 0.f;
+  // As in the other kernel: 0 for a row that sees no key, NaN for one whose logits are all -inf.
+  const bool sees = min(nk, nk - nq + tok - q_lo + 1) > 0;
+  const float inv = none ? (sees ? NAN : 0.f) : 1.f / w_all;
   __nv_bfloat16* dst = a.O + (long long)tok * a.o_row + (long long)head * D + lane * kPer;
 #pragma unroll
   for (int k = 0; k < kPer; k += 2)
     *reinterpret_cast<__nv_bfloat162*>(dst + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[row] = m > -INFINITY ? (m + log2f(w_all)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[row] = none ? (sees ? NAN : -INFINITY) : (m + log2f(w_all)) * 0.6931471805599453f;
 }
 
 // The form and the number of key shares for a call, by mean lengths (the lengths

@@ -185,6 +185,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// The larger of two, NaN if one of them is (fmaxf gives the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // 2^x for a pair on the FMA pipe, for -126 <= x (smaller arguments give 2^-126) and
 // x < 127: x = n + r with n the nearest integer, taken from the low bits of
 // x + 1.5 2^23, and 2^r by a polynomial of degree 4, the minimax fit of the

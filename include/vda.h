@@ -426,7 +426,9 @@ vda_status vda_static_workspace_poll(void* stream);
  * memory, not decreasing, within 0 .. the tensor's tokens. The host never reads
  * them; values out of that range are clamped to it (wrong rows, no access out of
  * range). Rows of tokens outside cu[0] .. cu[N]-1 are never read into a result
- * and never written. Within a sequence the values are expected to be finite.
+ * and never written. Within a sequence the values are expected to be finite:
+ * one that is not is never taken for a finite one, but it may also reach rows of
+ * its sequence that do not see its token (as 0 x NaN).
  *
  * Token tensors hold one row per token, [heads, d] contiguous within it; the
  * distance between rows is given in elements (q_row, ...), so that a slice of
@@ -460,7 +462,8 @@ vda_status vda_causal_attention_workspace(const vda_attention_config* cfg, size_
  * 0 .. nk - nq + r:
  *   o_r = sum_j p_rj v_j,  p_rj = exp(scale q_r.k_j) / sum_j' exp(scale q_r.k_j'),
  * query head h with key head h / (Hq / Hkv). A query that sees no key gives 0
- * (and lse = -infinity). With nq = 1 it is the step of generation: one new token
+ * (and lse = -infinity); one that sees a logit of NaN or +infinity, or none but
+ * -infinity, gives NaN (and lse = NaN). With nq = 1 it is the step of generation: one new token
  * of each sequence against its cache.
  *   Q, O   [Tq, Hq, d] bf16       K, V  [Tk, Hkv, d] bf16
  *   cu_q, cu_k  int32 [N + 1]: the sequences' rows of Q (O) and of K (V)
