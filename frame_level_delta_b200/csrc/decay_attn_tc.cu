@@ -107,7 +107,7 @@ struct DaJob {
 struct DaArgs {
   int N, H, T, njobs;
   int seg;                  // chunks per segment
-  int items;                // entries of seg_state: segments of all sequences, at most
+  int items;                // entries of seg_state: segments of the sequences that have several, at most
   const int* cu;
   const float* log_decay;   // [H]
   DaJob job[kMaxJobs];
@@ -133,24 +133,26 @@ __device__ __forceinline__ void chunk_tokens(int len, int reverse, int p0, int p
   hi = min(len, reverse ? (nch - p0) * kC : p1 * kC);
 }
 
-// Segments of the sequences before sequence sq: where its own begin in seg_state.
-// Every thread of the block calls it; up to 32 sequences each warp counts by itself.
+// Segments of sequence i, where it has several: a sequence of one has no entry in seg_state.
+__device__ __forceinline__ int cut_segments(const DaArgs& a, int i, int seg_tokens) {
+  int lo, hi;
+  seq::bounds(a.cu, i, a.T, lo, hi);
+  const int n = (hi - lo + seg_tokens - 1) / seg_tokens;
+  return n > 1 ? n : 0;
+}
+
+// Those of the sequences before sequence sq: where its own begin in seg_state. Every
+// thread of the block calls it; up to 32 sequences each warp counts by itself.
 __device__ __forceinline__ int segments_before(const DaArgs& a, int sq, int* scratch) {
   const int seg_tokens = a.seg * kC;
   if (a.N <= 32) {
-    int lo = 0, hi = 0;
     const int lane = threadIdx.x % 32;
-    if (lane < sq) seq::bounds(a.cu, lane, a.T, lo, hi);
-    return (int)__reduce_add_sync(0xffffffffu, lane < sq ? max(1, (hi - lo + seg_tokens - 1) / seg_tokens) : 0);
+    return (int)__reduce_add_sync(0xffffffffu, lane < sq ? cut_segments(a, lane, seg_tokens) : 0);
   }
   if (threadIdx.x == 0) *scratch = 0;
   __syncthreads();
   int n = 0;
-  for (int i = threadIdx.x; i < sq; i += blockDim.x) {
-    int lo, hi;
-    seq::bounds(a.cu, i, a.T, lo, hi);
-    n += max(1, (hi - lo + seg_tokens - 1) / seg_tokens);
-  }
+  for (int i = threadIdx.x; i < sq; i += blockDim.x) n += cut_segments(a, i, seg_tokens);
   if (n) atomicAdd(scratch, n);
   __syncthreads();
   return *scratch;
@@ -959,7 +961,13 @@ int segment_chunks(const vda_decay_config& c, int njobs) {
   const long long share = ((chunks + c.N / 2) * c.H * njobs + 147) / 148;
   return (int)std::min<long long>(1 << 20, std::max<long long>(kMinSegChunks, share));
 }
+// Segments of all sequences, at most.
 long long segment_items(const vda_decay_config& c, int seg) { return (long long)c.T / ((long long)seg * kC) + c.N; }
+// Those of the sequences that have several: a sequence of x > 1 segments' tokens has
+// ceil(x) <= 2 floor(x), and the floors together are at most the tensor's.
+long long state_items(const vda_decay_config& c, int seg) {
+  return std::min(segment_items(c, seg), 2 * ((long long)c.T / ((long long)seg * kC)));
+}
 
 template <int D>
 cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr[4], const long long row[4], int nmaps,
@@ -968,7 +976,7 @@ cudaError_t launch_d(const vda_decay_config& c, DaArgs& a, const void* const ptr
   a.seg = segment_chunks(c, a.njobs);
   const bool whole = (long long)c.T <= (long long)a.seg * kC;  // no sequence can be longer than a segment
   const long long items = segment_items(c, a.seg);
-  a.items = (int)items;
+  a.items = (int)state_items(c, a.seg);
   a.seg_state = whole ? nullptr : static_cast<float*>(ws);
   a.wait_ns = 2000000000u;
   const long long grid = items * c.H * a.njobs;
@@ -1008,7 +1016,7 @@ size_t decay_attention_workspace(const vda_decay_config& c, bool backward) {
   const int njobs = backward ? 3 : 1;
   const int seg = segment_chunks(c, njobs);
   if ((long long)c.T <= (long long)seg * kC) return 0;
-  return (size_t)segment_items(c, seg) * c.H * njobs * c.d * c.d * sizeof(float);
+  return (size_t)state_items(c, seg) * c.H * njobs * c.d * c.d * sizeof(float);
 }
 
 cudaError_t launch_decay_attention(const vda_decay_config& c, const void* Q, const void* K, const void* V,
