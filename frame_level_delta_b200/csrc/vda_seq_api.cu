@@ -14,11 +14,18 @@ namespace vda {
 
 namespace {
 
+// Word 0 is the status, word kTaken what the last poll took from it.
 __device__ __align__(256) uint32_t g_sequence_status[64];
+constexpr int kTaken = 32;
 
 constexpr int kMaxDevices = 64;
 std::atomic<void*> g_status_addr[kMaxDevices];
 std::mutex g_status_mu;
+std::mutex g_poll_mu;
+
+// Reads the word and clears it in one step: what another stream's kernel reports
+// meanwhile is either taken or left for the next poll.
+__global__ void take_status_kernel(uint32_t* word) { word[kTaken] = atomicExch(word, 0u); }
 
 }  // namespace
 
@@ -225,16 +232,27 @@ vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void*
   return of(e);
 }
 
+vda_status vda_selftest_sequence_wait(uint64_t spins, void* stream) {
+  uint32_t* word = nullptr;
+  cudaError_t e = sequence_status(&word);
+  if (e == cudaSuccess) e = launch_selftest_wait(word, spins, static_cast<cudaStream_t>(stream));
+  return of(e);
+}
+
 vda_status vda_sequence_poll(void* stream) {
   uint32_t* word = nullptr;
   if (sequence_status(&word) != cudaSuccess) return VDA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return VDA_ERR_CUDA;
+  // One poll at a time: kTaken is one word. The stream's work is done, so the wait below is short.
+  std::lock_guard<std::mutex> lock(g_poll_mu);
   uint32_t v = 0;
-  cudaError_t e = cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, s);
+  take_status_kernel<<<1, 1, 0, s>>>(word);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word + kTaken, sizeof(v), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return VDA_ERR_CUDA;
-  if (v == 0) return VDA_OK;
-  return cudaMemsetAsync(word, 0, sizeof(v), s) == cudaSuccess ? VDA_ERR_TIMEOUT : VDA_ERR_CUDA;
+  return v == 0 ? VDA_OK : VDA_ERR_TIMEOUT;
 }
 
 }  // extern "C"

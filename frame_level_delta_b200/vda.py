@@ -44,7 +44,7 @@ EXPORTS = ["vda_create", "vda_destroy", "vda_workspace_size", "vda_prepare", "vd
            "vda_causal_attention_workspace", "vda_causal_attention", "vda_causal_attention_backward_workspace",
            "vda_causal_attention_backward", "vda_decay_attention_workspace", "vda_decay_attention",
            "vda_decay_attention_step", "vda_decay_attention_backward_workspace", "vda_decay_attention_backward",
-           "vda_sequence_poll"]
+           "vda_sequence_poll", "vda_selftest_sequence_wait"]
 
 
 class VDAError(RuntimeError):
@@ -128,6 +128,7 @@ def lib() -> ctypes.CDLL:
         L.vda_decay_attention_backward_workspace.argtypes = [dcfg, szp]
         L.vda_decay_attention_backward.argtypes = [dcfg] + [vp] * 13 + [sz, vp]
         L.vda_sequence_poll.argtypes = [vp]
+        L.vda_selftest_sequence_wait.argtypes = [ctypes.c_uint64, vp]
         for name in EXPORTS:
             if name not in ("vda_status_string", "vda_last_error", "vda_static_workspace_capacity"):
                 getattr(L, name).restype = ctypes.c_int
@@ -900,6 +901,11 @@ def sequence_poll(stream=None) -> int:
     """Status of the prompt path's calls on the current device since the last poll
     (synchronises the stream; VDA_ERR_TIMEOUT if a device-side wait gave up)."""
     return lib().vda_sequence_poll(_stream_handle(stream))
+
+
+def selftest_sequence_wait(spins: int, stream=None) -> int:
+    """A bounded wait that gives up and reports to the word sequence_poll reads."""
+    return lib().vda_selftest_sequence_wait(spins, _stream_handle(stream))
 
 
 def to_device(inp: Dict[str, torch.Tensor], device="cuda") -> Dict[str, torch.Tensor]:

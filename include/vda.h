@@ -545,11 +545,16 @@ vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void*
 /*
  * Status of the prompt path's calls on the current device: synchronise `stream`,
  * and return VDA_ERR_TIMEOUT if a bounded device-side wait of any of them gave up
- * since the last poll (the word is cleared), VDA_OK otherwise. The word is kept
+ * since the last poll, VDA_OK otherwise. Reading the word clears it, in one step:
+ * of polls at the same time one reports. The word is kept
  * by the library, one per device; the first of these calls on a device looks its
  * address up, so make that one before any stream capture.
  */
 vda_status vda_sequence_poll(void* stream);
+
+/* vda_selftest_bounded_wait on the word that vda_sequence_poll reads: the next poll
+ * reports VDA_ERR_TIMEOUT. */
+vda_status vda_selftest_sequence_wait(uint64_t spins, void* stream);
 
 #ifdef __cplusplus
 }
