@@ -108,6 +108,46 @@ vda_status of(cudaError_t e) {
   return e == cudaSuccess ? VDA_OK : e == cudaErrorInvalidConfiguration ? VDA_ERR_UNSUPPORTED : VDA_ERR_CUDA;
 }
 
+// Rows of a tensor in memory: `count` of `width` bytes, `row` bytes apart.
+struct Rows {
+  const void* p;
+  long long count, row, width;
+};
+Rows tokens(const void* p, long long count, long long row, long long width) { return {p, count, row * 2, width * 2}; }
+Rows flat(const void* p, long long bytes) { return {p, 1, bytes, bytes}; }
+
+// Whether two of them share a byte. Parts of one tensor (heads of a joint projection) lie
+// between one another without sharing any.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.count < 1 || b.count < 1 || a.width < 1 || b.width < 1) return false;
+  const unsigned long long pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  auto end = [](unsigned long long p, const Rows& r) { return p + (unsigned long long)((r.count - 1) * r.row + r.width); };
+  if (end(pa, a) <= pb || end(pb, b) <= pa) return false;
+  if (a.count == 1 && b.count == 1) return true;
+  if (a.row == b.row) {
+    const long long at = (long long)(pb - pa) % a.row, off = at < 0 ? at + a.row : at;  // b's start within a's rows
+    if (off >= a.width && a.row - off >= b.width) return false;
+  }
+  for (long long i = 0, j = 0; i < a.count && j < b.count;) {
+    const unsigned long long x = pa + i * a.row, y = pb + j * b.row;
+    if (x + a.width <= y) ++i;
+    else if (y + b.width <= x) ++j;
+    else return true;
+  }
+  return false;
+}
+
+// Outputs may not share memory with inputs or with one another.
+bool outputs_overlap(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  for (const Rows* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Rows& i : ins)
+      if (overlap(*o, i)) return true;
+    for (const Rows* p = o + 1; p != outs.end(); ++p)
+      if (overlap(*o, *p)) return true;
+  }
+  return false;
+}
+
 // What becomes of states when there is no token at all: the state stays.
 cudaError_t keep_state(const vda_decay_config& c, const float* from, float* to, cudaStream_t s) {
   if (!to || to == from) return cudaSuccess;
@@ -135,6 +175,11 @@ vda_status vda_causal_attention(const vda_attention_config* cfg, const void* Q, 
     return VDA_ERR_INVALID_ARG;
   if (!all_aligned({Q, K, V, O}, 16) || !all_aligned({cu_q, cu_k, k_len, lse}, 4)) return VDA_ERR_ALIGNMENT;
   if ((st = check_ws(workspace, workspace_bytes, causal_attention_workspace(*cfg))) != VDA_OK) return st;
+  const long long wq = (long long)cfg->Hq * cfg->d, wk = (long long)cfg->Hkv * cfg->d;
+  if (outputs_overlap({tokens(O, cfg->Tq, cfg->o_row, wq), flat(lse, 4LL * cfg->Tq * cfg->Hq)},
+                      {tokens(Q, cfg->Tq, cfg->q_row, wq), tokens(K, cfg->Tk, cfg->k_row, wk),
+                       tokens(V, cfg->Tk, cfg->v_row, wk)}))
+    return VDA_ERR_INVALID_ARG;
   if (cfg->Tq == 0) return VDA_OK;
   uint32_t* status = nullptr;
   cudaError_t e = sequence_status(&status);
@@ -163,6 +208,12 @@ vda_status vda_causal_attention_backward(const vda_attention_config* cfg, const 
   if (!all_aligned({Q, K, V, O, dO, dQ, dK, dV}, 16) || !all_aligned({cu_q, cu_k, k_len, lse}, 4))
     return VDA_ERR_ALIGNMENT;
   if ((st = check_ws(workspace, workspace_bytes, causal_attention_backward_workspace(*cfg))) != VDA_OK) return st;
+  const long long wq = (long long)cfg->Hq * cfg->d, wk = (long long)cfg->Hkv * cfg->d;
+  if (outputs_overlap({tokens(dQ, cfg->Tq, wq, wq), tokens(dK, cfg->Tk, wk, wk), tokens(dV, cfg->Tk, wk, wk)},
+                      {tokens(Q, cfg->Tq, cfg->q_row, wq), tokens(K, cfg->Tk, cfg->k_row, wk),
+                       tokens(V, cfg->Tk, cfg->v_row, wk), tokens(O, cfg->Tq, cfg->o_row, wq),
+                       tokens(dO, cfg->Tq, cfg->o_row, wq), flat(lse, 4LL * cfg->Tq * cfg->Hq)}))
+    return VDA_ERR_INVALID_ARG;
   if (cfg->Tq == 0 && cfg->Tk == 0) return VDA_OK;
   uint32_t* status = nullptr;
   cudaError_t e = sequence_status(&status);
@@ -187,6 +238,11 @@ vda_status vda_decay_attention(const vda_decay_config* cfg, const void* Q, const
   if (any_null({log_decay, cu}) || (cfg->T > 0 && any_null({Q, K, V, O}))) return VDA_ERR_INVALID_ARG;
   if (!all_aligned({Q, K, V, O, S0, S}, 16) || !all_aligned({log_decay, cu}, 4)) return VDA_ERR_ALIGNMENT;
   if ((st = check_ws(workspace, workspace_bytes, decay_attention_workspace(*cfg, false))) != VDA_OK) return st;
+  const long long w = (long long)cfg->H * cfg->d, states = 4LL * cfg->N * w * cfg->d;
+  if (outputs_overlap({tokens(O, cfg->T, cfg->o_row, w), flat(S, states)},
+                      {tokens(Q, cfg->T, cfg->q_row, w), tokens(K, cfg->T, cfg->k_row, w),
+                       tokens(V, cfg->T, cfg->v_row, w), flat(S == S0 ? nullptr : S0, states)}))
+    return VDA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cfg->T == 0) return of(keep_state(*cfg, S0, S, s));
   uint32_t* status = nullptr;
@@ -201,6 +257,11 @@ vda_status vda_decay_attention_step(const vda_decay_config* cfg, const void* Q, 
   if (st != VDA_OK) return st;
   if (cfg->T != cfg->N || any_null({Q, K, V, log_decay, S, O})) return VDA_ERR_INVALID_ARG;
   if (!all_aligned({Q, K, V, O, S}, 16) || !all_aligned({log_decay}, 4)) return VDA_ERR_ALIGNMENT;
+  const long long w = (long long)cfg->H * cfg->d;
+  if (outputs_overlap({tokens(O, cfg->T, cfg->o_row, w), flat(S, 4LL * cfg->N * w * cfg->d)},
+                      {tokens(Q, cfg->T, cfg->q_row, w), tokens(K, cfg->T, cfg->k_row, w),
+                       tokens(V, cfg->T, cfg->v_row, w)}))
+    return VDA_ERR_INVALID_ARG;
   return of(launch_decay_step(*cfg, Q, K, V, log_decay, S, O, static_cast<cudaStream_t>(stream)));
 }
 
@@ -218,10 +279,15 @@ vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void*
   vda_status st = check_prompt(cfg);
   if (st != VDA_OK) return st;
   if (any_null({log_decay, cu}) || (cfg->T > 0 && any_null({Q, K, V, dO, dQ, dK, dV}))) return VDA_ERR_INVALID_ARG;
-  if (dS0 && (dS0 == dS || dS0 == S0)) return VDA_ERR_INVALID_ARG;
   if (!all_aligned({Q, K, V, dO, dQ, dK, dV, S0, dS, dS0}, 16) || !all_aligned({log_decay, cu}, 4))
     return VDA_ERR_ALIGNMENT;
   if ((st = check_ws(workspace, workspace_bytes, decay_attention_workspace(*cfg, true))) != VDA_OK) return st;
+  const long long w = (long long)cfg->H * cfg->d, states = 4LL * cfg->N * w * cfg->d;
+  if (outputs_overlap({tokens(dQ, cfg->T, w, w), tokens(dK, cfg->T, w, w), tokens(dV, cfg->T, w, w), flat(dS0, states)},
+                      {tokens(Q, cfg->T, cfg->q_row, w), tokens(K, cfg->T, cfg->k_row, w),
+                       tokens(V, cfg->T, cfg->v_row, w), tokens(dO, cfg->T, cfg->o_row, w), flat(S0, states),
+                       flat(dS, states)}))
+    return VDA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cfg->T == 0) return of(keep_state(*cfg, dS, dS0, s));
   uint32_t* status = nullptr;

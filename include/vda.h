@@ -437,8 +437,10 @@ vda_status vda_static_workspace_poll(void* stream);
  * aligned. bf16 storage, d 64 or 128, every sum and state in fp32.
  *
  * These calls take no context and keep no device memory. They only enqueue work;
- * all argument errors come back before any launch. Outputs may not overlap inputs,
- * but where a call says so. Calls that may run at the
+ * all argument errors come back before any launch. An output that shares memory
+ * with an input or with another output is refused (VDA_ERR_INVALID_ARG), but
+ * where a call allows it; parts of one tensor that lie between one another
+ * without sharing any are not refused. Calls that may run at the
  * same time need separate workspaces. vda_sequence_poll reads the status of
  * their bounded waits.
  */
@@ -535,7 +537,7 @@ vda_status vda_decay_attention_backward_workspace(const vda_decay_config* cfg, s
  * heads' fixed factors: they get no gradient.
  *   dO          [T, H, d] bf16, rows o_row apart
  *   dQ, dK, dV  [T, H, d] bf16, contiguous; rows outside the sequences are left
- *   dS, dS0     float32 [N, H, d, d]; dS0 may not be dS or S0
+ *   dS, dS0     float32 [N, H, d, d]
  */
 vda_status vda_decay_attention_backward(const vda_decay_config* cfg, const void* Q, const void* K, const void* V,
                                         const void* dO, const float* log_decay, const int32_t* cu, const float* S0,
