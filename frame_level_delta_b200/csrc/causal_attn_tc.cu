@@ -13,7 +13,8 @@
 //
 // An SM works on two tiles at a time, so that the tensor cores have one's products
 // while the other's exponentials run. Each tile has eight softmax warps (two threads to
-// a row, half the keys each; with four warps a packed batch took 6% longer), its logits
+// a row, half the keys each; with four a packed batch took 6% longer when the second four
+// were added), its logits
 // S and its accumulator O in TMEM (128 and D columns; the probabilities overwrite their
 // logits as packed bf16). The two are streams of one CTA that share each key block
 // (long prompts at d = 128, where the reads of K and V count), or two CTAs of one
@@ -52,10 +53,19 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kMinSplitBlocks = 4;
-constexpr int kFewRows = 32;  // 48 ragged caches: 133 us with whole tiles, 129 so
-// CTAs per SM that the split form aims at. Measured with 48 ragged caches of up to 8192 slots,
-// 32 / 8 heads (16; 32 of them): two 163 (76; 114) us, three 139 (73; 115), four 138 (74; 120),
-// five 138 (80; 120), eight 146 (83; 125).
+// Times in this file are of calls behind one another in a captured graph, under lasting load
+// (about 1.7 GHz; in short bursts the longer ones take 9 to 13% less), with
+// inputs larger than L2.
+//
+// Rows of a tile in the split form where sequences have few, which makes room for a third block
+// in flight. In us, with such tiles (with whole ones): 8 caches of 4096 slots, four tokens each,
+// 32 / 8 heads 27 (30); 16 of up to 8192, eight tokens each, 32 / 8 heads, d = 64 48 (53); one
+// token each: 16 of up to 8192, 8 / 1 heads, d = 64 19 (20); 48 of up to 8192, 32 / 8 heads 121
+// (119), 8 / 8 heads 160 (157), at d = 64 101 (96).
+constexpr int kFewRows = 32;
+// CTAs per SM that the split form aims at. 48 ragged caches of up to 8192 slots, 32 / 8 heads
+// (16; 32 of them): two 127 (45; 82) us, three 121 (45; 82), four 121 (47; 83), five 121
+// (47; 84), eight 128 (53; 92).
 constexpr int kSplitCtas = 4;
 constexpr int kShortKeys = 2304;  // d = 128: mean keys below which a CTA has one stream
 constexpr uint32_t kFma = 0x22;  // pairs of eight whose exponentials the FMA pipe takes
@@ -456,9 +466,10 @@ __global__ void __launch_bounds__((CaCfg<D, kStreams, kFew>::kThreads), 3 - kStr
         for (int q = 0; q < 4; ++q) ls2[q] = make_float2(0.f, 0.f);
         // Two of eight pairs on the FMA pipe: the exponentials of two streams
         // would keep the special-function units as long as the products keep the
-        // tensor cores (packed batch: none so 115.6 us, one 112.9, two 112.5, three
-        // 113.3, four 113.9). Not in masked blocks (its smallest value is not 0), where 32 keys
-        // that no row of the warp sees are left out.
+        // tensor cores (packed batch, and 8191 tokens: none so 125.7 and 551 us, one 124.2
+        // and 550, two 124.5 and 548, three 126.1 and 554, four 126.5 and 566). Not in masked
+        // blocks (its smallest value is not 0), where 32 keys that no row of the warp sees
+        // are left out.
         auto weights = [&](auto plain) {
 #pragma unroll
           for (int c2 = 0; c2 < 2; ++c2) {
@@ -643,10 +654,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const CaArgs a) {
 //  - d = 64, and short sequences at d = 128: one stream a CTA, two CTAs to an SM: one's
 //    start and end hide behind the other's blocks.
 //  - Else two streams a CTA, which halves the reads of K and V.
-// Measured at d = 128, 24 / 8 heads, one stream (two): 16 x 256 tokens 33.1 (41.9) us,
-// 16 x 512 73.4 (86.0), 8 x 1024 92.5 (100), 8 x 1536 164 (172), 6 x 2048 195 (203),
-// 4 x 3000 253 (243), 2 x 4096 221 (206); at d = 64, 8 / 8 heads: 16 x 512 24.4 (26.7), 8 x 1536 55.9
-// (60.5), 2 x 4096 66.1 (67.0).
+// Measured at d = 128, 24 / 8 heads, one stream (two): 16 x 256 tokens 34.6 (44.9) us,
+// 16 x 512 75.6 (86.7), 8 x 1024 101 (102), 8 x 1536 188 (186), 6 x 2048 226 (224; in a short
+// burst 197 and 205), 4 x 3000 298 (279), 2 x 4096 260 (240); at d = 64, 8 / 8 heads: 16 x 512
+// 25.8 (28.1), 8 x 1536 57.2 (62.1), 2 x 4096 67.2 (68.1).
 struct Plan {
   int streams;
   bool split;

@@ -953,8 +953,9 @@ constexpr int kWholeChunks = 9;
 // kMinSegChunks (a segment reads its keys and values twice, and the launch that
 // forms the segments' states costs its start). Up to kWholeChunks in all, nothing is
 // cut: the two launches more cost what the shorter chain saves (one sequence of 24
-// heads, d = 128, in segments of 4: 6 chunks 37 us, 12 chunks 39; uncut 26 and 42; at
-// d = 64 27 and 28 against 20 and 33).
+// heads, d = 128, uncut, and in segments of 4: 6 chunks 27.5 and 32.6 us, 9 chunks 37.0
+// and 33.3, 12 chunks 46.6 and 36.4; at d = 64 21.0 and 23.4, 28.8 and 26.1, 36.2 and
+// 27.0: the two meet between 7 and 8).
 int segment_chunks(const vda_decay_config& c, int njobs) {
   const long long chunks = ((long long)c.T + kC - 1) / kC;
   if (chunks <= kWholeChunks) return kWholeChunks;

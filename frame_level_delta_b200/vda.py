@@ -560,7 +560,12 @@ def selftest_bounded_wait(status: torch.Tensor, spins: int, stream=None) -> int:
 # tokens cu[i] .. cu[i+1]-1 are sequence i's. Token tensors are [tokens, heads, d]
 # bf16 with contiguous heads and any distance between tokens (a slice of the
 # heads, a part of a joint projection); outputs made here are contiguous, and
-# their rows outside the sequences stay uninitialised.
+# their rows outside the sequences stay uninitialised. An output given by the caller
+# may lie between an input's rows, but not share memory with it.
+#
+# As everywhere in this binding, no call takes part in autograd: results carry no
+# history, whatever their inputs require, and gradients are calls of their own. A
+# program that trains wraps the pairs in a torch.autograd.Function.
 
 
 def _rows(name: str, t, shape: tuple, dev) -> int:
@@ -708,7 +713,8 @@ def causal_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: to
     The last query of a sequence stands at its last key, so one query per sequence
     against a cache (cu_k: the caches' rooms, k_len: their filled parts) is a step
     of generation. ``scale`` defaults to 1 / sqrt(d). Returns O, or (O, lse) with
-    lse [Tq, Hq] float32."""
+    lse [Tq, Hq] float32; neither has autograd history (causal_attention_backward
+    gives the gradients)."""
     key = _signature(Q, K, V, cu_q, cu_k, k_len, O)
     key = key and ("attention", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(key, _check_attention(Q, K, V, cu_q, cu_k, k_len, scale, O))
@@ -799,7 +805,8 @@ def decay_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, log_decay
     (vda_decay_attention): S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T,
     o_t = scale S_t q_t. Q, K, V [T, H, d] bf16, d 64 or 128; log_decay [H]
     float32; S0 [N, H, d, d] float32, zero if not given. Returns O and the states
-    after each sequence (``S`` may be S0: updated in place)."""
+    after each sequence (``S`` may be S0: updated in place), without autograd history
+    (decay_attention_backward gives the gradients)."""
     key = _signature(Q, K, V, log_decay, cu, S0, O, S)
     key = key and ("decay", key, _number(scale))
     c, dev, n = _checked.get(key) or _remember(key, _check_decay(Q, K, V, log_decay, cu, S0, scale, O, S))
